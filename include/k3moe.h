@@ -279,6 +279,120 @@ k3moe_status k3moe_layer_cached(k3moe_cache *cache, const void *x, int32_t T, co
                                 size_t ws_bytes, void *stream);
 
 /*
+ * Routing from given logits, for routers other than the layer's own: softmax
+ * or sigmoid scores, a balance bias on the scores, groups of experts, top-k,
+ * renormalised and scaled weights.  Per token, with l its E logits:
+ *   s_e = softmax(l)_e or 1 / (1 + exp(-l_e))           the score
+ *   c_e = s_e + bias_e with a bias; without one the experts are ranked by
+ *         their logits, which order them as their scores do
+ *   An expert is out when its logit is -inf or NaN, or its c_e is -inf or NaN.
+ *   groups: with n_groups > 1 the experts form n_groups runs of
+ *         n_experts / n_groups consecutive ids; a group's value is the sum of
+ *         its group_top largest c_e (-inf if it has fewer experts left; with
+ *         group_top 2 and no bias the sum of the two scores); the
+ *         groups_kept groups of the largest value stay (ties to the lower
+ *         group), the experts of the others are out
+ *   idx = the top_k experts left with the largest c_e, ties to the lower id,
+ *         listed in descending order; -1 where no expert is left
+ *   weight_j = s_idx_j, divided by the sum of the token's top_k scores with
+ *         K3MOE_RENORM_TOPK (0 where that sum is 0), times weight_scale; 0
+ *         where idx is -1
+ * A softmax is taken over every expert whose logit is not -inf; a NaN or
+ * +inf logit makes the token's softmax scores NaN, as the formula does.
+ * The selection is exact: c_e and the groups' values are compared as 64-bit
+ * values computed from the logits and the bias as given, so equal inputs tie
+ * and near ties are decided as the formula says.  Weights are fp32.
+ *
+ * logits: fp32, or bf16 with K3MOE_LOGITS_BF16, [T] rows of n_experts, ld
+ *   elements from one row to the next (0: n_experts); aligned to their size.
+ * bias: fp32 [E] or NULL.  idx: int32 [T][top_k], weight: fp32 [T][top_k].
+ * 1 <= n_experts <= 1024; 1 <= top_k <= min(n_experts, 32); 1 <= n_groups <=
+ * 32 dividing n_experts; 1 <= groups_kept <= n_groups; group_top 1 or 2, at
+ * most n_experts / n_groups; top_k <= groups_kept * n_experts / n_groups;
+ * weight_scale finite.  No workspace; one launch.
+ */
+#define K3MOE_SCORE_SOFTMAX 0
+#define K3MOE_SCORE_SIGMOID 1
+#define K3MOE_LOGITS_BF16 64u /* k3moe_gate: the logits are bf16 */
+typedef struct {
+    int32_t n_experts;
+    int32_t top_k;
+    int32_t score;       /* K3MOE_SCORE_SOFTMAX or K3MOE_SCORE_SIGMOID */
+    int32_t n_groups;    /* 1: no groups */
+    int32_t groups_kept;
+    int32_t group_top;
+    float weight_scale;
+    uint32_t flags;      /* K3MOE_RENORM_TOPK | K3MOE_LOGITS_BF16 */
+} k3moe_gate_desc;
+k3moe_status k3moe_gate(const void *logits, int64_t ld, int32_t T, const float *bias,
+                        const k3moe_gate_desc *gate, int32_t *idx, float *weight, void *stream);
+
+/*
+ * k3moe_layer under a given routing (k3moe_gate's, or any other):
+ *   y[t] = S(x_t) + sum_j weight[t][j] o_idx[t][j](x_t)
+ * idx: int32 [T][top_k], weight: fp32 [T][top_k], 4-byte aligned.  idx -1
+ * (any negative value) is no expert: the pair adds nothing and its weight is
+ * not read.  The same expert may stand in several places of a token's row: its weights
+ * add up.  An id of n_experts or more records K3MOE_ERR_DEVICE_CHECK in the
+ * workspace status and counts as no expert.  The weights are used as given
+ * (K3MOE_RENORM_TOPK and K3MOE_BIAS_SELECT_ONLY have no effect here), and
+ * decode passes run the separate launches also with K3MOE_ONE_LAUNCH.
+ * Expert blobs that no token picks are not read and may be NULL.  Everything
+ * else is as for k3moe_layer, the workspace and its size included; idx and
+ * weight must not overlap the workspace.
+ */
+k3moe_status k3moe_layer_routed(const void *x, int32_t T, const int32_t *idx, const float *weight,
+                                const uint8_t *const *expert_blobs, const void *shared_wg,
+                                const void *shared_wu, const void *shared_wd,
+                                const k3moe_dims *dims, void *y, void *ws, size_t ws_bytes,
+                                void *stream);
+
+/*
+ * Dense product of bf16 activations and weights with its epilogue: the bf16
+ * router of k3moe_gate (fp32 output), the projections and the dense
+ * feed-forward blocks around the layer.  Per token t and output column n:
+ *   v[t][n]   = sum_k x[t][k] w[n][k] + bias[n]
+ *   out[t][n] = act(v[t][n]) + residual[t][n]                    w_gate NULL
+ *   out[t][n] = act(g[t][n]) * v[t][n] + residual[t][n]          gated, with
+ *   g[t][n]   = sum_k x[t][k] w_gate[n][k] + bias_gate[n]
+ * act: K3MOE_ACT_NONE, _RELU, _SILU (v / (1 + exp(-v))), _GELU (v times the
+ * normal distribution function of v), _GELU_TANH (its tanh approximation).
+ * Products are exact, sums and the epilogue fp32, one rounding at the end.
+ *
+ * x: bf16, T rows of k elements, ldx elements from row to row; w, w_gate:
+ *   bf16, n rows of k elements, ldw from row to row (both alike); bias,
+ *   bias_gate: fp32 [n] or NULL (bias_gate only with w_gate); residual (may be
+ *   NULL): T rows of n elements of out's type, ldr; out: T rows of n elements,
+ *   bf16 or fp32 with K3MOE_OUT_FP32, ldo.  A row distance of 0 means rows
+ *   without gaps.  residual may be out itself (in place, ldr == ldo); no
+ *   other overlap with out is allowed.
+ * 1 <= n, 8 <= k, both at most 2^24; k, ldx and ldw multiples of 8; x, w and
+ *   w_gate 16-byte aligned; bias, bias_gate 4-byte aligned; residual and out
+ *   aligned to their element size (16-byte aligned rows are stored and read
+ *   with wider accesses).
+ * ws: device scratch of k3moe_linear_workspace_size() bytes for the call's T
+ *   or a larger one, 256-byte aligned and zero-filled before its first use;
+ *   it starts with a status word for k3moe_device_status, and must not be
+ *   used by two calls that may run at the same time.
+ */
+#define K3MOE_ACT_NONE 0
+#define K3MOE_ACT_RELU 1
+#define K3MOE_ACT_SILU 2
+#define K3MOE_ACT_GELU 3
+#define K3MOE_ACT_GELU_TANH 4
+typedef struct {
+    int32_t n;      /* output columns */
+    int32_t k;      /* reduction length */
+    int32_t act;    /* K3MOE_ACT_* */
+    uint32_t flags; /* K3MOE_OUT_FP32 */
+} k3moe_linear_desc;
+size_t k3moe_linear_workspace_size(const k3moe_linear_desc *lin, int32_t T_max);
+k3moe_status k3moe_linear(const void *x, int64_t ldx, int32_t T, const void *w, const void *w_gate,
+                          int64_t ldw, const float *bias, const float *bias_gate,
+                          const void *residual, int64_t ldr, const k3moe_linear_desc *lin,
+                          void *out, int64_t ldo, void *ws, size_t ws_bytes, void *stream);
+
+/*
  * k3moe_layer with the activations in HOST memory: copies x_host ([T][d]
  * bf16) into the workspace, runs the layer, and copies y back to y_host
  * ([T][d], bf16 or fp32 per flags), all ordered on `stream` (the copies are

@@ -29,6 +29,16 @@ K3MOE_STRICT = 4
 K3MOE_RENORM_TOPK = 8
 K3MOE_BIAS_SELECT_ONLY = 16
 K3MOE_ONE_LAUNCH = 32
+K3MOE_LOGITS_BF16 = 64
+
+K3MOE_SCORE_SOFTMAX = 0
+K3MOE_SCORE_SIGMOID = 1
+
+K3MOE_ACT_NONE = 0
+K3MOE_ACT_RELU = 1
+K3MOE_ACT_SILU = 2
+K3MOE_ACT_GELU = 3
+K3MOE_ACT_GELU_TANH = 4
 
 
 class K3moeError(RuntimeError):
@@ -51,6 +61,25 @@ def make_dims(d, ff, n_experts, top_k, ff_shared, flags=0) -> k3moe_dims:
     return k3moe_dims(d, ff, n_experts, top_k, ff_shared, flags)
 
 
+class k3moe_gate_desc(ctypes.Structure):
+    _fields_ = [("n_experts", ctypes.c_int32), ("top_k", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("n_groups", ctypes.c_int32), ("groups_kept", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("weight_scale", ctypes.c_float), ("flags", ctypes.c_uint32)]
+
+
+def make_gate(n_experts, top_k, score=K3MOE_SCORE_SOFTMAX, n_groups=1, groups_kept=1, group_top=1,
+              weight_scale=1.0, flags=0) -> k3moe_gate_desc:
+    return k3moe_gate_desc(n_experts, top_k, score, n_groups, groups_kept, group_top, weight_scale, flags)
+
+
+class k3moe_linear_desc(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("k", ctypes.c_int32), ("act", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+def make_linear(n, k, act=K3MOE_ACT_NONE, flags=0) -> k3moe_linear_desc:
+    return k3moe_linear_desc(n, k, act, flags)
+
+
 class k3moe_cache_stats(ctypes.Structure):
     _fields_ = [("requests", ctypes.c_uint64), ("hits", ctypes.c_uint64), ("fills", ctypes.c_uint64),
                 ("evictions", ctypes.c_uint64)]
@@ -63,7 +92,9 @@ if not os.path.exists(LIB_PATH):
 lib = ctypes.CDLL(LIB_PATH)
 
 _vp, _i32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+_i64 = ctypes.c_int64
 _dp = ctypes.POINTER(k3moe_dims)
+_gp, _lp = ctypes.POINTER(k3moe_gate_desc), ctypes.POINTER(k3moe_linear_desc)
 _SIGS = {
     "k3moe_abi_version": ([], ctypes.c_int),
     "k3moe_blob_bytes": ([_dp], _sz),
@@ -80,6 +111,11 @@ _SIGS = {
     "k3moe_layer_timed": ([_vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _dp, _vp, _vp, _sz, _vp,
                            ctypes.POINTER(_vp), _i32, ctypes.POINTER(_i32)], ctypes.c_int),
     "k3moe_layer_noalloc": ([_vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _dp, _vp, _vp], ctypes.c_int),
+    "k3moe_gate": ([_vp, _i64, _i32, _vp, _gp, _vp, _vp, _vp], ctypes.c_int),
+    "k3moe_layer_routed": ([_vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _dp, _vp, _vp, _sz, _vp], ctypes.c_int),
+    "k3moe_linear_workspace_size": ([_lp, _i32], _sz),
+    "k3moe_linear": ([_vp, _i64, _i32, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _lp, _vp, _i64, _vp, _sz, _vp],
+                     ctypes.c_int),
     "k3moe_device_status": ([_vp, _vp], ctypes.c_int),
     "k3moe_status_string": ([ctypes.c_int], ctypes.c_char_p),
     "k3moe_last_error": ([], ctypes.c_char_p),
@@ -204,6 +240,68 @@ def k3moe_layer_timed(x, T, w_router, bias, expert_blobs, shared_wg, shared_wu, 
                                ctypes.byref(dims), _ptr(y), _ptr(ws), ws_bytes, _stream(stream),
                                arr, len(events), ctypes.byref(nk))
     return st, nk.value
+
+
+def _rows(t, sizes, cols):
+    """Row distance of a 2-D operand given as a tensor (0: rows without gaps);
+    -1, which the library refuses, when the tensor is not `cols` wide with
+    consecutive elements of one of the given sizes in bytes."""
+    if t is None or isinstance(t, int):
+        return 0
+    if t.element_size() not in sizes or t.shape[-1] != cols or (cols > 1 and t.stride(-1) != 1):
+        return -1
+    if t.dim() == 1 or t.shape[0] == 1:
+        return cols if t.dim() < 3 else -1
+    return t.stride(0) if t.dim() == 2 and t.stride(0) >= cols else -1
+
+
+def _flat(*ts) -> bool:
+    """Whether every tensor given is contiguous and of 4-byte elements."""
+    return all(t is None or isinstance(t, int) or (t.element_size() == 4 and t.is_contiguous()) for t in ts)
+
+
+def k3moe_gate(logits, T, bias, gate, idx, weight, stream=None) -> int:
+    """logits: [T, E] tensor (rows may be a slice of wider ones) or an address."""
+    ld = _rows(logits, (2,) if gate.flags & K3MOE_LOGITS_BF16 else (4,), gate.n_experts)
+    if ld < 0 or not _flat(bias, idx, weight):
+        return K3MOE_ERR_INVALID_ARGUMENT
+    return lib.k3moe_gate(_ptr(logits), ld, T, _ptr(bias), ctypes.byref(gate), _ptr(idx), _ptr(weight),
+                          _stream(stream))
+
+
+def k3moe_layer_routed(x, T, idx, weight, expert_blobs, shared_wg, shared_wu, shared_wd, dims, y, ws,
+                       ws_bytes=None, stream=None) -> int:
+    if not _flat(idx, weight):
+        return K3MOE_ERR_INVALID_ARGUMENT
+    ws_bytes = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
+    return lib.k3moe_layer_routed(_ptr(x), T, _ptr(idx), _ptr(weight), _ptr(expert_blobs), _ptr(shared_wg),
+                                  _ptr(shared_wu), _ptr(shared_wd), ctypes.byref(dims), _ptr(y), _ptr(ws), ws_bytes,
+                                  _stream(stream))
+
+
+def k3moe_linear_workspace_size(lin: k3moe_linear_desc, T_max: int) -> int:
+    return lib.k3moe_linear_workspace_size(ctypes.byref(lin), T_max)
+
+
+def k3moe_linear(x, T, w, w_gate, bias, bias_gate, residual, lin, out, ws, ws_bytes=None, stream=None) -> int:
+    """Tensors (x, w, w_gate, residual, out) may be slices of wider rows."""
+    osz = (4,) if lin.flags & K3MOE_OUT_FP32 else (2,)
+    ldx, ldw, ldr, ldo = _rows(x, (2,), lin.k), _rows(w, (2,), lin.k), _rows(residual, osz, lin.n), _rows(out, osz, lin.n)
+    if min(ldx, ldw, ldr, ldo) < 0 or not _flat(bias, bias_gate) or (w_gate is not None
+                                                                    and _rows(w_gate, (2,), lin.k) != ldw):
+        return K3MOE_ERR_INVALID_ARGUMENT
+    ws_bytes = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
+    return lib.k3moe_linear(_ptr(x), ldx, T, _ptr(w), _ptr(w_gate), ldw, _ptr(bias), _ptr(bias_gate), _ptr(residual),
+                            ldr, ctypes.byref(lin), _ptr(out), ldo, _ptr(ws), ws_bytes, _stream(stream))
+
+
+def new_linear_workspace(lin: k3moe_linear_desc, T_max: int, device="cuda"):
+    """A zero-filled workspace tensor (uint8) for k3moe_linear."""
+    import torch
+    n = k3moe_linear_workspace_size(lin, T_max)
+    if n == 0:
+        raise K3moeError(K3MOE_ERR_UNSUPPORTED_SHAPE, "k3moe_linear_workspace_size")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
 def k3moe_device_status(ws, stream=None) -> int:

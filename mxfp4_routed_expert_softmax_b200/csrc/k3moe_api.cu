@@ -15,11 +15,14 @@
 #include "common.cuh"
 #include "decode_kernels.cuh"
 #include "expert_cache.cuh"
+#include "gate_kernels.cuh"
 #include "k3moe.h"
 #include "layer_kernel.cuh"
 #include "layout.cuh"
+#include "linear_kernels.cuh"
 #include "prefill_kernels.cuh"
 #include "prefill_router_mma.cuh"
+#include "routed_kernels.cuh"
 
 namespace {
 
@@ -414,13 +417,33 @@ cudaError_t launch_layer_route(const DeviceInfo &di, const RouteParams &rp, int 
     return launch_layer(di, lp, nst, st);
 }
 
+// A routing given by the caller (k3moe_layer_routed): [T][k] each.
+struct GivenRouting {
+    const int32_t *idx;
+    const float *weight;
+};
+
+// The checks and the dispatch of a given routing for one decode pass, and its
+// activation pieces: CTA 0 dispatches, the others take one 32-column block of
+// x per warp.  grid_out: the CTAs that count on prep_done (all of them).
+cudaError_t launch_given(const DeviceInfo &di, const RouteParams &rp, const GivenRouting &g, cudaStream_t st,
+                         int *grid_out) {
+    const int warps = kGivenThreads / 32;
+    int grid = 1 + (rp.Tc * (rp.d / 32) + warps - 1) / warps;
+    if (grid > di.sms) grid = di.sms;
+    *grid_out = grid;
+    const GivenParams gp{rp, g.idx, g.weight};
+    return launch(given_setup_kernel, dim3(grid), dim3(kGivenThreads), 0, st, false, gp);
+}
+
 // Launches of the grouped prefill, pass after pass; rp carries the shapes,
 // blobs and tensor-map templates.  routing_only: stop after the top-k.
 // norm_w (non-null): x holds the residual stream h; the layer runs on
 // RMSNorm(h) (written into the pass's xn region) and h is added to its output.
+// given (non-null): the routing is the caller's, no router runs.
 k3moe_status prefill_impl(DeviceInfo &di, RouteParams rp, const k3moe_dims *dims, const uint16_t *x, int T,
                           void *y, int32_t *idx_out, float *w_out, cudaStream_t st, bool routing_only = false,
-                          const uint16_t *norm_w = nullptr, float eps = 0.f) {
+                          const uint16_t *norm_w = nullptr, float eps = 0.f, const GivenRouting *given = nullptr) {
     const int d = dims->d, E = dims->n_experts, k = dims->top_k;
     const int ffs = rp.has_shared ? dims->ff_shared : 0;
     const bool out32 = (dims->flags & K3MOE_OUT_FP32) != 0;
@@ -430,7 +453,7 @@ k3moe_status prefill_impl(DeviceInfo &di, RouteParams rp, const k3moe_dims *dims
     cudaError_t e;
     // the router as three exact bf16 parts, once per call, and their tensor maps
     RouterMmaParams rm{};
-    {
+    if (!given) {
         uint16_t *w1 = reinterpret_cast<uint16_t *>(wsb + P.wsplit);
         const size_t n = (size_t)E * d;
         const RouterSplitParams spp{rp.wr, n, w1, w1 + n, w1 + 2 * n};
@@ -466,8 +489,18 @@ k3moe_status prefill_impl(DeviceInfo &di, RouteParams rp, const k3moe_dims *dims
         pp.ngs = ffs > 0 ? ceil_div(Tq, kGroup) : 0;
         pp.ff = dims->ff;
         pp.ffs = ffs;
-        // router: tiles of 128 experts x 128 tokens on the tensor cores
-        {
+        if (given) {
+            const PfGivenParams gp{given->idx + (size_t)t0 * k,
+                                   given->weight + (size_t)t0 * k,
+                                   Tq, E, k,
+                                   reinterpret_cast<int32_t *>(wsb + P.idx),
+                                   reinterpret_cast<float *>(wsb + P.wt),
+                                   reinterpret_cast<WsHeader *>(wsb + rp.L.hdr)};
+            const int per = kGivenThreads / 32;
+            e = launch(pf_given_kernel, dim3(ceil_div(Tq, per)), dim3(kGivenThreads), 0, st, false, gp);
+            if (e != cudaSuccess) return cuda_fail(e, "given routing launch");
+        } else {
+            // router: tiles of 128 experts x 128 tokens on the tensor cores
             k3moe_status s = tmap_bf16_rows(pp.r.x, d, Tq, rm.tx);
             if (s != K3MOE_OK) return s;
             rm.T = Tq;
@@ -476,9 +509,9 @@ k3moe_status prefill_impl(DeviceInfo &di, RouteParams rp, const k3moe_dims *dims
             e = launch(pf_router_mma_kernel, dim3(tiles < di.sms ? tiles : di.sms), dim3(kRmThreads), rm_smem_bytes(),
                        st, false, rm);
             if (e != cudaSuccess) return cuda_fail(e, "prefill router launch");
+            e = launch(pf_topk_kernel, dim3(Tq), dim3(kRouteThreads), 0, st, false, pp);
+            if (e != cudaSuccess) return cuda_fail(e, "prefill top-k launch");
         }
-        e = launch(pf_topk_kernel, dim3(Tq), dim3(kRouteThreads), 0, st, false, pp);
-        if (e != cudaSuccess) return cuda_fail(e, "prefill top-k launch");
         if (routing_only) continue;
         const int nhb = ceil_div(Tq, kPfHistTok);
         e = launch(pf_hist_kernel, dim3(nhb), dim3(kRouteThreads), 0, st, false, pp);
@@ -520,6 +553,7 @@ k3moe_status prefill_impl(DeviceInfo &di, RouteParams rp, const k3moe_dims *dims
         cp.out_fp32 = out32;
         cp.y = reinterpret_cast<uint8_t *>(y) + (size_t)t0 * d * (out32 ? 4 : 2);
         cp.resid = norm_w ? x + (size_t)t0 * d : nullptr;
+        cp.idx = given ? reinterpret_cast<const int32_t *>(wsb + P.idx) : nullptr;
         e = launch(pf_combine_kernel, dim3(4 * di.sms), dim3(256), 0, st, false, cp);
         if (e != cudaSuccess) return cuda_fail(e, "prefill combine launch");
     }
@@ -544,7 +578,8 @@ k3moe_status layer_impl(const void *x, int32_t T, const float *w_router, const f
                         const void *shared_wu, const void *shared_wd, const k3moe_dims *dims,
                         void *y, int32_t *idx_out, float *w_out, void *ws, size_t ws_bytes,
                         void *stream, const void *x_host, void *y_host, EventHook *hook = nullptr,
-                        const uint16_t *norm_w = nullptr, float eps = 0.f, int layer_mode = kLayerFull) {
+                        const uint16_t *norm_w = nullptr, float eps = 0.f, int layer_mode = kLayerFull,
+                        const GivenRouting *given = nullptr) {
     k3moe_status s = check_dims(dims);
     if (s != K3MOE_OK) return s;
     const bool from_host = x_host != nullptr;
@@ -552,8 +587,8 @@ k3moe_status layer_impl(const void *x, int32_t T, const float *w_router, const f
     if (!from_host && (!x || !y || !aligned(x, 16) || !aligned(y, 16)))
         return K3MOE_ERR_INVALID_ARGUMENT;
     if (from_host && !y_host) return K3MOE_ERR_INVALID_ARGUMENT;
-    if (!w_router || !aligned(w_router, 16) || !expert_blobs || !aligned(expert_blobs, 8))
-        return K3MOE_ERR_INVALID_ARGUMENT;
+    if (!expert_blobs || !aligned(expert_blobs, 8)) return K3MOE_ERR_INVALID_ARGUMENT;
+    if (!given && (!w_router || !aligned(w_router, 16))) return K3MOE_ERR_INVALID_ARGUMENT;
     if (bias && !aligned(bias, 4)) return K3MOE_ERR_INVALID_ARGUMENT;
     if ((idx_out && !aligned(idx_out, 4)) || (w_out && !aligned(w_out, 4)))
         return K3MOE_ERR_INVALID_ARGUMENT;
@@ -619,7 +654,7 @@ k3moe_status layer_impl(const void *x, int32_t T, const float *w_router, const f
             y = ystage;
         }
         s = prefill_impl(*di, rp, dims, reinterpret_cast<const uint16_t *>(x), T, y, idx_out, w_out, st, false,
-                         norm_w, eps);
+                         norm_w, eps, given);
         if (s != K3MOE_OK) return s;
         if (from_host) {
             e = cudaMemcpyAsync(y_host, ystage, (size_t)T * d * ybytes, cudaMemcpyDeviceToHost, st);
@@ -667,7 +702,8 @@ k3moe_status layer_impl(const void *x, int32_t T, const float *w_router, const f
         EventHook none;
         EventHook &hk = hook ? *hook : none;
         if ((e = hk.record(st)) != cudaSuccess) return cuda_fail(e);
-        const int lst = (one_launch(dims) || layer_mode != kLayerFull) ? layer_stages(*di, dims, Tc) : 0;
+        const int lst =
+            !given && (one_launch(dims) || layer_mode != kLayerFull) ? layer_stages(*di, dims, Tc) : 0;
         if (layer_mode != kLayerFull && lst == 0) return K3MOE_ERR_UNSUPPORTED_SHAPE;
         if (lst > 0) {
             // the whole pass in one launch
@@ -707,7 +743,12 @@ k3moe_status layer_impl(const void *x, int32_t T, const float *w_router, const f
             rp.x = reinterpret_cast<const uint16_t *>(wsb + L.xn);
         }
         int route_ctas = 0;
-        e = launch_route(*di, rp, st, &route_ctas);
+        if (given) {
+            const GivenRouting g{given->idx + (size_t)c0 * dims->top_k, given->weight + (size_t)c0 * dims->top_k};
+            e = launch_given(*di, rp, g, st, &route_ctas);
+        } else {
+            e = launch_route(*di, rp, st, &route_ctas);
+        }
         if (e != cudaSuccess) return cuda_fail(e, "router launch");
         if ((e = hk.record(st)) != cudaSuccess) return cuda_fail(e);
 
@@ -740,6 +781,28 @@ k3moe_status layer_impl(const void *x, int32_t T, const float *w_router, const f
             if (e != cudaSuccess) return cuda_fail(e);
         }
     }
+    return K3MOE_OK;
+}
+
+k3moe_status check_gate(const k3moe_gate_desc *g) {
+    if (!g) return K3MOE_ERR_INVALID_ARGUMENT;
+    if (g->flags & ~(K3MOE_RENORM_TOPK | K3MOE_LOGITS_BF16)) return K3MOE_ERR_INVALID_ARGUMENT;
+    if (g->n_experts < 1 || g->n_experts > kGateMaxE) return K3MOE_ERR_UNSUPPORTED_SHAPE;
+    if (g->score != K3MOE_SCORE_SOFTMAX && g->score != K3MOE_SCORE_SIGMOID) return K3MOE_ERR_INVALID_ARGUMENT;
+    if (g->n_groups < 1 || g->n_groups > 32 || g->n_experts % g->n_groups) return K3MOE_ERR_UNSUPPORTED_SHAPE;
+    const int size = g->n_experts / g->n_groups;
+    if (g->groups_kept < 1 || g->groups_kept > g->n_groups || g->group_top < 1 || g->group_top > 2 ||
+        g->group_top > size || g->top_k < 1 || g->top_k > kGateMaxK || g->top_k > g->groups_kept * size)
+        return K3MOE_ERR_INVALID_ARGUMENT;
+    if (!(g->weight_scale - g->weight_scale == 0.f)) return K3MOE_ERR_INVALID_ARGUMENT;  // infinite or NaN
+    return K3MOE_OK;
+}
+
+k3moe_status check_linear(const k3moe_linear_desc *l) {
+    if (!l) return K3MOE_ERR_INVALID_ARGUMENT;
+    if (l->flags & ~K3MOE_OUT_FP32 || l->act < K3MOE_ACT_NONE || l->act > K3MOE_ACT_GELU_TANH)
+        return K3MOE_ERR_INVALID_ARGUMENT;
+    if (l->n < 1 || l->n > (1 << 24) || l->k < 8 || l->k > (1 << 24) || l->k % 8) return K3MOE_ERR_UNSUPPORTED_SHAPE;
     return K3MOE_OK;
 }
 
@@ -1117,6 +1180,94 @@ k3moe_status k3moe_layer_cached(k3moe_cache *cache, const void *x, int32_t T, co
         if (s != K3MOE_OK) return s;
     }
     return K3MOE_OK;
+}
+
+k3moe_status k3moe_gate(const void *logits, int64_t ld, int32_t T, const float *bias, const k3moe_gate_desc *gate,
+                        int32_t *idx, float *weight, void *stream) {
+    k3moe_status s = check_gate(gate);
+    if (s != K3MOE_OK) return s;
+    const bool bf16 = (gate->flags & K3MOE_LOGITS_BF16) != 0;
+    if (ld == 0) ld = gate->n_experts;
+    if (T < 1 || ld < gate->n_experts || !logits || !aligned(logits, bf16 ? 2 : 4) || !idx || !aligned(idx, 4) ||
+        !weight || !aligned(weight, 4) || (bias && !aligned(bias, 4)))
+        return K3MOE_ERR_INVALID_ARGUMENT;
+    GateParams p{};
+    p.logits = logits;
+    p.ld = ld;
+    p.T = T;
+    p.E = gate->n_experts;
+    p.k = gate->top_k;
+    p.bias = bias;
+    p.sigmoid = gate->score == K3MOE_SCORE_SIGMOID;
+    p.groups = gate->groups_kept == gate->n_groups ? 1 : gate->n_groups;  // every group kept: no groups
+    p.kept = gate->groups_kept;
+    p.group_top = gate->group_top;
+    p.renorm = (gate->flags & K3MOE_RENORM_TOPK) != 0;
+    p.bf16 = bf16;
+    p.scale = gate->weight_scale;
+    p.idx = idx;
+    p.weight = weight;
+    cudaError_t e = launch(gate_kernel, dim3(T < 65536 ? T : 65536), dim3(32), 0, reinterpret_cast<cudaStream_t>(stream),
+                           false, p);
+    return e == cudaSuccess ? K3MOE_OK : cuda_fail(e, "gate launch");
+}
+
+k3moe_status k3moe_layer_routed(const void *x, int32_t T, const int32_t *idx, const float *weight,
+                                const uint8_t *const *expert_blobs, const void *shared_wg, const void *shared_wu,
+                                const void *shared_wd, const k3moe_dims *dims, void *y, void *ws, size_t ws_bytes,
+                                void *stream) {
+    if (!idx || !aligned(idx, 4) || !weight || !aligned(weight, 4)) return K3MOE_ERR_INVALID_ARGUMENT;
+    const GivenRouting g{idx, weight};
+    return layer_impl(x, T, nullptr, nullptr, expert_blobs, shared_wg, shared_wu, shared_wd, dims, y, nullptr, nullptr,
+                      ws, ws_bytes, stream, nullptr, nullptr, nullptr, nullptr, 0.f, kLayerFull, &g);
+}
+
+size_t k3moe_linear_workspace_size(const k3moe_linear_desc *lin, int32_t T_max) {
+    if (check_linear(lin) != K3MOE_OK || T_max < 1) return 0;
+    return sizeof(WsHeader);
+}
+
+k3moe_status k3moe_linear(const void *x, int64_t ldx, int32_t T, const void *w, const void *w_gate, int64_t ldw,
+                          const float *bias, const float *bias_gate, const void *residual, int64_t ldr,
+                          const k3moe_linear_desc *lin, void *out, int64_t ldo, void *ws, size_t ws_bytes,
+                          void *stream) {
+    k3moe_status s = check_linear(lin);
+    if (s != K3MOE_OK) return s;
+    const int n = lin->n, k = lin->k;
+    const bool out32 = (lin->flags & K3MOE_OUT_FP32) != 0;
+    const size_t osz = out32 ? 4 : 2;
+    if (ldx == 0) ldx = k;
+    if (ldw == 0) ldw = k;
+    if (ldr == 0) ldr = n;
+    if (ldo == 0) ldo = n;
+    if (T < 1 || !x || !aligned(x, 16) || !w || !aligned(w, 16) || (w_gate && !aligned(w_gate, 16)) || !out ||
+        !aligned(out, osz) || (residual && !aligned(residual, osz)) || (bias && !aligned(bias, 4)) ||
+        (bias_gate && (!w_gate || !aligned(bias_gate, 4))))
+        return K3MOE_ERR_INVALID_ARGUMENT;
+    if (ldx < k || ldx % 8 || ldw < k || ldw % 8 || ldr < n || ldo < n || (residual == out && ldr != ldo))
+        return K3MOE_ERR_INVALID_ARGUMENT;
+    if (!ws || !aligned(ws, 256)) return K3MOE_ERR_INVALID_ARGUMENT;
+    if (ws_bytes < k3moe_linear_workspace_size(lin, T)) return K3MOE_ERR_WORKSPACE_TOO_SMALL;
+    LinearParams p{};
+    p.x = reinterpret_cast<const uint16_t *>(x);
+    p.w = reinterpret_cast<const uint16_t *>(w);
+    p.wg = reinterpret_cast<const uint16_t *>(w_gate);
+    p.bias = bias;
+    p.bias_g = bias_gate;
+    p.resid = residual;
+    p.out = out;
+    p.ldx = ldx;
+    p.ldw = ldw;
+    p.ldr = ldr;
+    p.ldo = ldo;
+    p.T = T;
+    p.N = n;
+    p.K = k;
+    p.act = lin->act;
+    p.out_fp32 = out32;
+    cudaError_t e = launch(linear_kernel, dim3(ceil_div(n, kLinN), ceil_div(T, kLinT)), dim3(256), 0,
+                           reinterpret_cast<cudaStream_t>(stream), false, p);
+    return e == cudaSuccess ? K3MOE_OK : cuda_fail(e, "linear launch");
 }
 
 k3moe_status k3moe_device_status(void *ws, void *stream) {

@@ -174,7 +174,8 @@ __global__ void __launch_bounds__(kRouteThreads) pf_hist_kernel(const __grid_con
     __syncthreads();
     const int t0 = blockIdx.x * kPfHistTok, t1 = min(p.T, t0 + kPfHistTok);
     const int32_t *idx = reinterpret_cast<const int32_t *>(p.r.ws + p.P.idx);
-    for (int i = t0 * k + threadIdx.x; i < t1 * k; i += blockDim.x) atomicAdd(&h[idx[i]], 1u);
+    for (int i = t0 * k + threadIdx.x; i < t1 * k; i += blockDim.x)
+        if (idx[i] >= 0) atomicAdd(&h[idx[i]], 1u);  // negative: no expert (given routings only)
     __syncthreads();
     uint32_t *hist = reinterpret_cast<uint32_t *>(p.r.ws + p.P.hist) + (size_t)blockIdx.x * E;
     for (int e = threadIdx.x; e < E; e += blockDim.x) hist[e] = h[e];
@@ -262,6 +263,10 @@ __global__ void __launch_bounds__(kRouteThreads) pf_place_kernel(const __grid_co
         uint32_t r = 0u;  // pairs of expert e at earlier tokens of the block (one per token at most)
         for (int q = 0; q < tl * k; ++q) r += s_idx[q] == e ? 1u : 0u;
         const int pid = (t0 + tl) * k + (i - tl * k);
+        if (e < 0) {
+            ploc[pid] = -1;
+            continue;
+        }
         const uint32_t rel = hist[e] + r;  // rank among expert e's pairs
         perm[eoff[e] + rel] = pid;
         pw[eoff[e] + rel] = wt[pid];
@@ -347,6 +352,7 @@ __global__ void __launch_bounds__(kRouteThreads) pf_prep_kernel(const __grid_con
         const int myloc = lane < k ? __ldcg(ploc + (size_t)t * k + lane) : 0;
         for (int j = 0; j < k; ++j) {
             const int loc = __shfl_sync(0xffffffffu, myloc, j);
+            if (loc < 0) continue;
             const int g = loc / kGroup, s = loc - g * kGroup;
             const size_t tb = (size_t)g * nkt + kt;
             uint8_t *tile = ws + p.P.xg + tb * kPfN * 128;
@@ -386,6 +392,7 @@ struct PfCombineParams {
     int T, d, k, has_shared, out_fp32;
     void *y;             // [T][d]
     const uint16_t *resid;  // bf16 [T][d] or null
+    const int32_t *idx;  // [T][k] of a given routing (negative: no output to add), or null: all are there
 };
 
 __global__ void pf_combine_kernel(const __grid_constant__ PfCombineParams p) {
@@ -394,9 +401,11 @@ __global__ void pf_combine_kernel(const __grid_constant__ PfCombineParams p) {
     for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (size_t)gridDim.x * blockDim.x) {
         const size_t t = i / nq, q = i - t * nq;
         const float4 *src = reinterpret_cast<const float4 *>(p.o + t * (size_t)(p.k + 1) * p.d) + q;
-        float4 s = __ldcs(src);
+        const int32_t *id = p.idx ? p.idx + t * p.k : nullptr;
+        float4 s = id && id[0] < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : __ldcs(src);
         const int ns = p.k + (p.has_shared ? 1 : 0);
         for (int j = 1; j < ns; ++j) {
+            if (id && j < p.k && id[j] < 0) continue;
             const float4 v = __ldcs(src + (size_t)j * nq);
             s.x += v.x;
             s.y += v.y;

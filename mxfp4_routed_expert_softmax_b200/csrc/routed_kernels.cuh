@@ -1,0 +1,163 @@
+// The layer under a given routing (k3moe_layer_routed): what stands in the
+// place of the router kernels.  Decode passes: one launch that checks the
+// given picks, merges repeated ones, writes the dispatch and the tensor maps
+// and quantises x; the gate/up and down kernels then run as after the router.
+// Grouped passes: the picks and weights, checked and merged, into the pass's
+// own tables, from which the sort by expert goes on.
+#pragma once
+
+#include "common.cuh"
+#include "decode_kernels.cuh"
+#include "layout.cuh"
+#include "prefill_kernels.cuh"
+
+namespace k3 {
+
+// One token's given picks, by one warp (lane j < k holds pick j): a negative
+// id, an id past the last expert (reported) and every repetition of an earlier
+// pick become -1, and the weight of a pick is the sum of the weights given to
+// its expert, in slot order.
+__device__ __forceinline__ void merge_picks(int &e, float &w, int k, int E, WsHeader *hdr) {
+    const int lane = threadIdx.x & 31;
+    if (lane >= k) e = -1;
+    if (e >= E) {
+        set_status(hdr, kStDeviceCheck);
+        e = -1;
+    }
+    if (e < 0) {
+        e = -1;
+        w = 0.f;
+    }
+    const uint32_t same = __match_any_sync(0xffffffffu, e);
+    const int first = __ffs(same) - 1;
+    float sum = 0.f;
+    for (int j = 0; j < k; ++j) {
+        const float wj = __shfl_sync(0xffffffffu, w, j);
+        if ((same >> j) & 1u) sum += wj;
+    }
+    const bool keep = e >= 0 && lane == first;
+    w = keep ? sum : 0.f;
+    e = keep ? e : -1;
+}
+
+constexpr int kGivenThreads = 256;
+constexpr int kGivenMaxE = 1024;
+
+struct GivenParams {
+    RouteParams r;         // shapes, blobs, tensor-map templates; x and Tc of this chunk
+    const int32_t *idx;    // given [Tc][k]
+    const float *weight;   // given [Tc][k]
+};
+
+// One decode pass (Tc <= kChunk).  CTA 0: warp t merges token t's picks; the
+// distinct experts in ascending id get the slots 0, 1, ... as the router's
+// dispatch orders them; the shared expert's and the selected experts' tensor
+// maps are rewritten where their pointers changed; the dispatch is released
+// for the down pass.  The other CTAs (all of them when there is one) quantise
+// x.  A chunk without any expert gets one slot with no blob and no token,
+// which the expert kernels take as an expert that adds nothing.
+__global__ void __launch_bounds__(kGivenThreads) given_setup_kernel(const __grid_constant__ GivenParams p) {
+    const RouteParams &r = p.r;
+    const Layout &L = r.L;
+    WsHeader *hdr = reinterpret_cast<WsHeader *>(r.ws + L.hdr);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int nwc = kGivenThreads / 32;
+    pdl_trigger();  // the gate/up pass waits for what it reads: x on prep_done, the rest on this grid
+    if (blockIdx.x > 0 || gridDim.x == 1) {
+        const int b0 = gridDim.x == 1 ? 0 : 1;
+        build_x_pieces(r.x, r.Tc, r.d, r.ws, L, (blockIdx.x - b0) * nwc + warp, (gridDim.x - b0) * nwc,
+                       r.has_shared != 0);
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) refresh_tmaps(r, r.E, 1);  // index E: the shared expert's maps
+    __syncthreads();
+    if (threadIdx.x == 0) red_add_release(&hdr->prep_done, 1u);  // this CTA's pieces (and the shared maps)
+    if (blockIdx.x > 0) return;
+    __shared__ uint32_t s_mask[kGivenMaxE];  // per expert: tokens that picked it
+    __shared__ uint32_t s_bits[32], s_pref[32];
+    for (int e = threadIdx.x; e < r.E; e += kGivenThreads) s_mask[e] = 0u;
+    if (threadIdx.x < 32) s_bits[threadIdx.x] = 0u;
+    __syncthreads();
+    int e = -1;
+    float w = 0.f;
+    if (warp < r.Tc) {
+        const bool in = lane < r.k;
+        e = in ? p.idx[warp * r.k + lane] : -1;
+        w = in && e >= 0 ? p.weight[warp * r.k + lane] : 0.f;
+        merge_picks(e, w, r.k, r.E, hdr);
+        if (in) {
+            reinterpret_cast<int32_t *>(r.ws + L.idx)[warp * r.k + lane] = e;
+            reinterpret_cast<float *>(r.ws + L.wt)[warp * r.k + lane] = w;
+        }
+        if (e >= 0) {
+            atomicOr(&s_mask[e], 1u << warp);
+            atomicOr(&s_bits[e >> 5], 1u << (e & 31));
+        }
+    }
+    __syncthreads();
+    if (warp == 0) {
+        const uint32_t c = __popc(s_bits[lane]);
+        uint32_t incl = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t n = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += n;
+        }
+        s_pref[lane] = incl - c;
+        if (lane == 31) hdr->n_unique = incl > 0u ? incl : 1u;
+        if (lane == 31 && incl == 0u) {
+            reinterpret_cast<const uint8_t **>(r.ws + L.uniq_blob)[0] = nullptr;
+            reinterpret_cast<int32_t *>(r.ws + L.uniq_eid)[0] = 0;
+            reinterpret_cast<uint32_t *>(r.ws + L.uniq_mask)[0] = 0u;
+        }
+    }
+    __syncthreads();
+    auto slot_of = [&](int x) { return (int)(s_pref[x >> 5] + __popc(s_bits[x >> 5] & ((1u << (x & 31)) - 1u))); };
+    if (e >= 0)
+        reinterpret_cast<int8_t *>(r.ws + L.uniq_slot)[(size_t)slot_of(e) * kChunk + warp] = (int8_t)lane;
+    const uint8_t **tc = reinterpret_cast<const uint8_t **>(r.ws + L.tcache);
+    for (int x = threadIdx.x; x < r.E; x += kGivenThreads) {
+        if (s_mask[x] == 0u) continue;
+        const int u = slot_of(x);
+        const uint8_t *b = r.blobs[x];
+        if (b == nullptr || (reinterpret_cast<uintptr_t>(b) & 15u) != 0u) {
+            set_status(hdr, kStDeviceCheck);
+            b = nullptr;
+        }
+        if (b != nullptr && tc[x] != b) {
+            write_expert_tmaps(r.ws, L, x, b, r.tmpl, r.scale_mask);
+            tc[x] = b;
+        }
+        reinterpret_cast<const uint8_t **>(r.ws + L.uniq_blob)[u] = b;
+        reinterpret_cast<int32_t *>(r.ws + L.uniq_eid)[u] = x;
+        reinterpret_cast<uint32_t *>(r.ws + L.uniq_mask)[u] = s_mask[x];
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) red_add_release(&hdr->disp_cnt, 1u);  // the dispatch is written
+}
+
+// A grouped pass: token by token (one warp each) the merged picks and weights
+// into the pass's tables.
+struct PfGivenParams {
+    const int32_t *idx;
+    const float *weight;
+    int T, E, k;
+    int32_t *idx_out;
+    float *w_out;
+    WsHeader *hdr;
+};
+__global__ void __launch_bounds__(kGivenThreads) pf_given_kernel(const __grid_constant__ PfGivenParams p) {
+    const int lane = threadIdx.x & 31;
+    const int t = blockIdx.x * (kGivenThreads / 32) + (threadIdx.x >> 5);
+    if (t >= p.T) return;
+    const size_t i = (size_t)t * p.k + lane;
+    const bool in = lane < p.k;
+    int e = in ? p.idx[i] : -1;
+    float w = in && e >= 0 ? p.weight[i] : 0.f;
+    merge_picks(e, w, p.k, p.E, p.hdr);
+    if (in) {
+        p.idx_out[i] = e;
+        p.w_out[i] = w;
+    }
+}
+
+}  // namespace k3
