@@ -5,6 +5,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cstdio>
 #include <new>
@@ -43,6 +44,8 @@ struct DeviceInfo {
     uint8_t *noalloc = nullptr;  // device address of g_noalloc_ws on this device, once set up
     int noalloc_shape[5] = {0, 0, 0, 0, 0};  // (d, ff, E, k, ff_shared) its layout was last used for
     int sms = 0;
+    int clusters[kLtMaxSplit + 1] = {};  // linear_tile_kernel clusters of this many CTAs that run at once
+    int pairs = 0;                       // linear_pair_kernel CTA pairs that run at once
 };
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_mu;
@@ -69,6 +72,23 @@ cudaError_t set_smem(Kern kernel, int bytes) {
 }
 
 
+// Clusters of n CTAs (kLtThreads threads, all of an SM's shared memory each)
+// that the device runs at the same time.
+template <typename Kern>
+cudaError_t max_clusters(Kern kernel, int n, int *out) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(n);
+    cfg.blockDim = dim3(kLtThreads);
+    cfg.dynamicSmemBytes = kSmemLimit;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = n;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(out, kernel, &cfg);
+}
+
 // One-time per-device set-up: SM count and the shared-memory opt-ins.
 k3moe_status device_info(DeviceInfo **out) {
     int dev = 0;
@@ -88,6 +108,12 @@ k3moe_status device_info(DeviceInfo **out) {
         if (r == cudaSuccess) r = set_smem(layer_kernel<1, true>, big);
         if (r == cudaSuccess) r = set_smem(layer_kernel<0, false>, big);
         if (r == cudaSuccess) r = set_smem(pf_router_mma_kernel, rm_smem_bytes());
+        if (r == cudaSuccess) r = set_smem(linear_tile_kernel<4>, big);
+        if (r == cudaSuccess) r = set_smem(linear_tile_kernel<8>, big);
+        if (r == cudaSuccess) r = set_smem(linear_pair_kernel, big);
+        for (int s = 2; s <= kLtMaxSplit && r == cudaSuccess; ++s)
+            r = max_clusters(linear_tile_kernel<4>, s, &di.clusters[s]);
+        if (r == cudaSuccess) r = max_clusters(linear_pair_kernel, 2, &di.pairs);
         if (r != cudaSuccess) return cuda_fail(r);
         di.ready = true;
     }
@@ -284,10 +310,11 @@ k3moe_status shared_tmaps(int d, int ffs, const void *wg, const void *wu, const 
     return K3MOE_OK;
 }
 
-// A 2-D tensor map of 16-bit elements [rows][cols] (row pitch cols * 2 bytes),
-// boxes of 64 columns x 128 rows with the 128-byte swizzle (the MMA's K-major
-// operand layout).
-k3moe_status tmap_bf16_rows(const void *addr, int cols, int rows, uint4 (&out)[8]) {
+// A 2-D tensor map of 16-bit elements [rows][cols] (rows ld elements apart, 0:
+// cols), boxes of 64 columns x `box` rows with the 128-byte swizzle (the MMA's
+// K-major operand layout).
+k3moe_status tmap_bf16_rows(const void *addr, int cols, int rows, uint4 (&out)[8], int64_t ld = 0,
+                            int box_rows = kRmTile) {
     std::lock_guard<std::mutex> lock(g_mu);
     static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
     if (!encode) {
@@ -303,8 +330,8 @@ k3moe_status tmap_bf16_rows(const void *addr, int cols, int rows, uint4 (&out)[8
     }
     CUtensorMap m;
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
-    const cuuint32_t box[2] = {(cuuint32_t)kRmKStep, (cuuint32_t)kRmTile};
+    const cuuint64_t strides[1] = {(cuuint64_t)(ld ? ld : cols) * 2};
+    const cuuint32_t box[2] = {(cuuint32_t)kRmKStep, (cuuint32_t)box_rows};
     const cuuint32_t es[2] = {1, 1};
     CUresult r = encode(&m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(addr), dims, strides, box, es,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -806,6 +833,130 @@ k3moe_status check_linear(const k3moe_linear_desc *l) {
     return K3MOE_OK;
 }
 
+// Launch with programmatic stream serialisation in clusters of n CTAs.
+template <typename Kern, typename P>
+cudaError_t launch_cluster(Kern kernel, int grid, int block, size_t smem, int n, cudaStream_t s, const P &params) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)n;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = n > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, params);
+}
+
+// -------------------------------------------------------- dense product --
+template <int RG, bool GATED, int TG>
+cudaError_t launch_stream(const LinearParams &p, cudaStream_t st) {
+    constexpr int NM = RG * (GATED ? 2 : 1), U = NM == 1 ? 8 / TG : 8 / (NM * TG) > 2 ? 8 / (NM * TG) : 2;
+    const int units = ceil_div(p.K, 64);
+    const int nw = units >= 64 ? 16 : units >= 8 ? 8 : 4;
+    return launch(linear_stream_kernel<RG, GATED, TG, U>, dim3(ceil_div(p.N, 8 * RG)), dim3(32 * nw),
+                  (size_t)nw * NM * TG * 64 * 4, st, true, p);
+}
+
+// 8 weight rows per CTA while that makes up to about six CTAs per SM, else 16
+// (each CTA reads all of x).
+cudaError_t linear_stream(const DeviceInfo &di, const LinearParams &p, cudaStream_t st) {
+    const bool wide = ceil_div(p.N, 8) > 4 * di.sms;
+    if (p.wg) {
+        if (p.T <= 8) return wide ? launch_stream<2, true, 1>(p, st) : launch_stream<1, true, 1>(p, st);
+        return wide ? launch_stream<2, true, 2>(p, st) : launch_stream<1, true, 2>(p, st);
+    }
+    if (p.T <= 8) return wide ? launch_stream<2, false, 1>(p, st) : launch_stream<1, false, 1>(p, st);
+    return wide ? launch_stream<2, false, 2>(p, st) : launch_stream<1, false, 2>(p, st);
+}
+
+k3moe_status linear_launch(const LinearParams &p, WsHeader *hdr, cudaStream_t st) {
+    DeviceInfo *di;
+    k3moe_status s = device_info(&di);
+    if (s != K3MOE_OK) return s;
+    cudaError_t e;
+    if (p.T <= kLsMaxT) {
+        e = linear_stream(*di, p, st);
+        return e == cudaSuccess ? K3MOE_OK : cuda_fail(e, "linear launch");
+    }
+    LinearTcParams a{};
+    a.p = p;
+    a.hdr = hdr;
+    a.wait_ns = wait_limit();
+    const bool gated = p.wg != nullptr;
+    const int nkt = ceil_div(p.K, kLtKStep);
+    // Estimated SM cycles of a K-step: the MMAs, or the operands' way from L2.
+    auto cost_tile = [&](int bn) { return std::max(2.0 * bn, (16384 + 128.0 * bn) / 48); };
+    auto cost_pair = [&](int bn) { return std::max(2.0 * bn, (16384 + 64.0 * bn) / 48); };
+    // one tile per cluster
+    const int nrb = ceil_div(p.N, gated ? 64 : 128);
+    double best = 1e300;
+    for (int bm = 128; bm <= 256; bm += 128) {
+        const int ntt = ceil_div(p.T, bm), bn = ceil_div(ceil_div(p.T, ntt), 16) * 16;
+        const long long units = (long long)nrb * ntt;
+        int split = 1;
+        for (int c = 2; c <= kLtMaxSplit && bn <= 128 && 2 * c <= nkt; ++c)
+            if (units <= di->clusters[c]) split = c;
+        const double waves = (double)((units * split + di->sms - 1) / di->sms);
+        const double cost = waves * (ceil_div(nkt, split) * cost_tile(bn) + 2000 + 16 * bn);
+        if (cost < best) {
+            best = cost;
+            a.bn = bn;
+            a.ntt = ntt;
+            a.split = split;
+        }
+    }
+    a.nrb = nrb;
+    bool pair = false;
+    if (!p.out_fp32) {
+        const int nrb2 = ceil_div(nrb, 2);
+        for (int bn = 64; bn <= 256; bn += 32) {
+            const int ntt = ceil_div(p.T, bn);
+            const long long items = (long long)nrb2 * ntt;
+            const double waves = (double)((items + di->pairs - 1) / di->pairs);
+            const double cost = waves * nkt * cost_pair(bn) + 4000 + 16 * bn;
+            if (cost < best) {
+                best = cost;
+                pair = true;
+                a.bn = bn;
+                a.ntt = ntt;
+                a.nrb = nrb2;
+            }
+        }
+    }
+    s = tmap_bf16_rows(p.w, p.K, p.N, a.tw, p.ldw, gated ? 64 : 128);
+    if (s == K3MOE_OK && gated) s = tmap_bf16_rows(p.wg, p.K, p.N, a.twg, p.ldw, 64);
+    if (s == K3MOE_OK) s = tmap_bf16_rows(p.x, p.K, p.T, a.tx, p.ldx, pair ? a.bn / 2 : a.bn);
+    if (s != K3MOE_OK) return s;
+    const int room = kSmemLimit - 1024 - kLtHead;
+    if (pair) {
+        const int sb = kLtA + a.bn * 64, ex = gated ? kLpExch : 0;
+        a.nst = std::min((room - ex) / sb, kLtMaxStages);
+        const int pairs = (int)std::min<long long>(di->pairs, (long long)a.nrb * a.ntt);
+        e = launch_cluster(linear_pair_kernel, 2 * pairs, kLtThreads, 1024 + kLtHead + a.nst * sb + ex, 2, st, a);
+        return e == cudaSuccess ? K3MOE_OK : cuda_fail(e, "linear launch");
+    }
+    const int sb = kLtA + a.bn * 128;
+    const int red = a.split * ceil_div(a.bn, a.split) * 512;
+    const bool own = a.split > 1;  // one CTA: the reduction buffer lies over the finished stages
+    a.nst = std::min((room - (own ? red : 0)) / sb, kLtMaxStages);
+    if (own) a.nst = std::min(a.nst, ceil_div(nkt, a.split));
+    a.red = kLtHead + (own ? a.nst * sb : 0);
+    a.chain = p.out_fp32 ? kLtChain : ceil_div(nkt, a.split);
+    const bool two = ceil_div(nkt, a.split) > a.chain;
+    a.tcols = 32;
+    while (a.tcols < (two ? 2 : 1) * a.bn) a.tcols *= 2;
+    const int bytes = 1024 + kLtHead + a.nst * sb + (own ? red : 0);
+    const int grid = a.nrb * a.ntt * a.split;
+    e = a.bn <= 128 ? launch_cluster(linear_tile_kernel<4>, grid, kLtThreads, bytes, a.split, st, a)
+                    : launch_cluster(linear_tile_kernel<8>, grid, kLtThreads, bytes, a.split, st, a);
+    return e == cudaSuccess ? K3MOE_OK : cuda_fail(e, "linear launch");
+}
+
 // Device address of the built-in scratch of k3moe_layer_noalloc on the
 // current device (looked up on the first use; the caller holds g_mu).
 k3moe_status noalloc_address(DeviceInfo &di) {
@@ -1240,6 +1391,7 @@ k3moe_status k3moe_linear(const void *x, int64_t ldx, int32_t T, const void *w, 
     if (ldw == 0) ldw = k;
     if (ldr == 0) ldr = n;
     if (ldo == 0) ldo = n;
+    if (T > kLinearMaxT) return K3MOE_ERR_UNSUPPORTED_SHAPE;
     if (T < 1 || !x || !aligned(x, 16) || !w || !aligned(w, 16) || (w_gate && !aligned(w_gate, 16)) || !out ||
         !aligned(out, osz) || (residual && !aligned(residual, osz)) || (bias && !aligned(bias, 4)) ||
         (bias_gate && (!w_gate || !aligned(bias_gate, 4))))
@@ -1265,9 +1417,7 @@ k3moe_status k3moe_linear(const void *x, int64_t ldx, int32_t T, const void *w, 
     p.K = k;
     p.act = lin->act;
     p.out_fp32 = out32;
-    cudaError_t e = launch(linear_kernel, dim3(ceil_div(n, kLinN), ceil_div(T, kLinT)), dim3(256), 0,
-                           reinterpret_cast<cudaStream_t>(stream), false, p);
-    return e == cudaSuccess ? K3MOE_OK : cuda_fail(e, "linear launch");
+    return linear_launch(p, reinterpret_cast<WsHeader *>(ws), reinterpret_cast<cudaStream_t>(stream));
 }
 
 k3moe_status k3moe_device_status(void *ws, void *stream) {
