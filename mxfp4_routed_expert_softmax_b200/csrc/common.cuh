@@ -126,6 +126,23 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity
     }
 }
 
+// The same for a converged warp, the answer alike in all lanes; gives up at
+// once when *abort is set, and sets it when the limit is reached.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, WsHeader *h, uint64_t limit_ns,
+                                               volatile int *abort) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const uint64_t t0 = globaltimer();
+    for (uint32_t i = 1;; ++i) {
+        if (__all_sync(0xffffffffu, mbar_try_wait_sleep(bar, parity))) return true;
+        if (__any_sync(0xffffffffu, *abort != 0)) return false;
+        if ((i & 63u) == 0u && __any_sync(0xffffffffu, globaltimer() - t0 > limit_ns)) {
+            set_status(h, kStTimeout);
+            *abort = 1;
+            return false;
+        }
+    }
+}
+
 // Wait (bounded, no status) for phase `parity` of `bar`: used on the way
 // out of a kernel whose pipeline gave up, so that bulk copies this thread
 // issued have landed before the CTA's shared memory is released.

@@ -108,11 +108,10 @@ k3moe_status device_info(DeviceInfo **out) {
         if (r == cudaSuccess) r = set_smem(layer_kernel<1, true>, big);
         if (r == cudaSuccess) r = set_smem(layer_kernel<0, false>, big);
         if (r == cudaSuccess) r = set_smem(pf_router_mma_kernel, rm_smem_bytes());
-        if (r == cudaSuccess) r = set_smem(linear_tile_kernel<4>, big);
-        if (r == cudaSuccess) r = set_smem(linear_tile_kernel<8>, big);
+        if (r == cudaSuccess) r = set_smem(linear_tile_kernel, big);
         if (r == cudaSuccess) r = set_smem(linear_pair_kernel, big);
         for (int s = 2; s <= kLtMaxSplit && r == cudaSuccess; ++s)
-            r = max_clusters(linear_tile_kernel<4>, s, &di.clusters[s]);
+            r = max_clusters(linear_tile_kernel, s, &di.clusters[s]);
         if (r == cudaSuccess) r = max_clusters(linear_pair_kernel, 2, &di.pairs);
         if (r != cudaSuccess) return cuda_fail(r);
         di.ready = true;
@@ -854,11 +853,13 @@ cudaError_t launch_cluster(Kern kernel, int grid, int block, size_t smem, int n,
 
 // -------------------------------------------------------- dense product --
 template <int RG, bool GATED, int TG>
-cudaError_t launch_stream(const LinearParams &p, cudaStream_t st) {
+cudaError_t launch_stream(const DeviceInfo &di, const LinearParams &p, cudaStream_t st) {
     constexpr int NM = RG * (GATED ? 2 : 1), U = NM == 1 ? 8 / TG : 8 / (NM * TG) > 2 ? 8 / (NM * TG) : 2;
     const int units = ceil_div(p.K, 64);
-    const int nw = units >= 64 ? 16 : units >= 8 ? 8 : 4;
-    return launch(linear_stream_kernel<RG, GATED, TG, U>, dim3(ceil_div(p.N, 8 * RG)), dim3(32 * nw),
+    const int ctas = ceil_div(p.N, 8 * RG);
+    // 16 warps fill an SM's registers: with more CTAs than SMs, 8 each
+    const int nw = units >= 64 && ctas <= di.sms ? 16 : units >= 8 ? 8 : 4;
+    return launch(linear_stream_kernel<RG, GATED, TG, U>, dim3(ctas), dim3(32 * nw),
                   (size_t)nw * NM * TG * 64 * 4, st, true, p);
 }
 
@@ -867,11 +868,11 @@ cudaError_t launch_stream(const LinearParams &p, cudaStream_t st) {
 cudaError_t linear_stream(const DeviceInfo &di, const LinearParams &p, cudaStream_t st) {
     const bool wide = ceil_div(p.N, 8) > 4 * di.sms;
     if (p.wg) {
-        if (p.T <= 8) return wide ? launch_stream<2, true, 1>(p, st) : launch_stream<1, true, 1>(p, st);
-        return wide ? launch_stream<2, true, 2>(p, st) : launch_stream<1, true, 2>(p, st);
+        if (p.T <= 8) return wide ? launch_stream<2, true, 1>(di, p, st) : launch_stream<1, true, 1>(di, p, st);
+        return wide ? launch_stream<2, true, 2>(di, p, st) : launch_stream<1, true, 2>(di, p, st);
     }
-    if (p.T <= 8) return wide ? launch_stream<2, false, 1>(p, st) : launch_stream<1, false, 1>(p, st);
-    return wide ? launch_stream<2, false, 2>(p, st) : launch_stream<1, false, 2>(p, st);
+    if (p.T <= 8) return wide ? launch_stream<2, false, 1>(di, p, st) : launch_stream<1, false, 1>(di, p, st);
+    return wide ? launch_stream<2, false, 2>(di, p, st) : launch_stream<1, false, 2>(di, p, st);
 }
 
 k3moe_status linear_launch(const LinearParams &p, WsHeader *hdr, cudaStream_t st) {
@@ -895,7 +896,8 @@ k3moe_status linear_launch(const LinearParams &p, WsHeader *hdr, cudaStream_t st
     // one tile per cluster
     const int nrb = ceil_div(p.N, gated ? 64 : 128);
     double best = 1e300;
-    for (int bm = 128; bm <= 256; bm += 128) {
+    const int chain = p.out_fp32 ? kLtChain : nkt;
+    for (int bm = 128; bm <= (nkt > chain ? 128 : 256); bm += 128) {
         const int ntt = ceil_div(p.T, bm), bn = ceil_div(ceil_div(p.T, ntt), 16) * 16;
         const long long units = (long long)nrb * ntt;
         int split = 1;
@@ -941,19 +943,19 @@ k3moe_status linear_launch(const LinearParams &p, WsHeader *hdr, cudaStream_t st
         return e == cudaSuccess ? K3MOE_OK : cuda_fail(e, "linear launch");
     }
     const int sb = kLtA + a.bn * 128;
-    const int red = a.split * ceil_div(a.bn, a.split) * 512;
-    const bool own = a.split > 1;  // one CTA: the reduction buffer lies over the finished stages
-    a.nst = std::min((room - (own ? red : 0)) / sb, kLtMaxStages);
-    if (own) a.nst = std::min(a.nst, ceil_div(nkt, a.split));
-    a.red = kLtHead + (own ? a.nst * sb : 0);
-    a.chain = p.out_fp32 ? kLtChain : ceil_div(nkt, a.split);
-    const bool two = ceil_div(nkt, a.split) > a.chain;
+    const int steps = ceil_div(nkt, a.split);
+    a.chain = std::min(chain, steps);
+    const bool chains = steps > a.chain;
+    // one CTA and one chain: the reduction buffer lies over the finished stages
+    const bool apart = a.split > 1 || chains;
+    const int red = (a.split * ceil_div(a.bn, a.split) + (a.split > 1 && chains ? a.bn : 0)) * 512;
+    a.nst = std::min((room - (apart ? red : 0)) / sb, kLtMaxStages);
+    if (apart) a.nst = std::min(a.nst, steps);
+    a.red = kLtHead + (apart ? a.nst * sb : 0);
     a.tcols = 32;
-    while (a.tcols < (two ? 2 : 1) * a.bn) a.tcols *= 2;
-    const int bytes = 1024 + kLtHead + a.nst * sb + (own ? red : 0);
-    const int grid = a.nrb * a.ntt * a.split;
-    e = a.bn <= 128 ? launch_cluster(linear_tile_kernel<4>, grid, kLtThreads, bytes, a.split, st, a)
-                    : launch_cluster(linear_tile_kernel<8>, grid, kLtThreads, bytes, a.split, st, a);
+    while (a.tcols < (chains ? 2 : 1) * a.bn) a.tcols *= 2;
+    const int bytes = 1024 + kLtHead + a.nst * sb + (apart ? red : 0);
+    e = launch_cluster(linear_tile_kernel, a.nrb * a.ntt * a.split, kLtThreads, bytes, a.split, st, a);
     return e == cudaSuccess ? K3MOE_OK : cuda_fail(e, "linear launch");
 }
 

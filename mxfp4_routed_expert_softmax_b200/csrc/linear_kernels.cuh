@@ -18,34 +18,74 @@ struct LinearParams {
     int T, N, K, act, out_fp32;
 };
 
-// The activation of one pre-activation value, in fp32.
-__device__ __forceinline__ float linear_act(float v, int act) {
-    switch (act) {
-        case K3MOE_ACT_RELU: return fmaxf(v, 0.f) + (v != v ? v : 0.f);
-        case K3MOE_ACT_SILU: return v / (1.0f + expf(-v));
-        case K3MOE_ACT_GELU: return 0.5f * v * erfcf(-0.70710678118654752f * v);
-        case K3MOE_ACT_GELU_TANH:
-            return 0.5f * v * (1.0f + tanhf(0.79788456080286536f * (v + 0.044715f * v * v * v)));
-        default: return v;
+// The activation of NV values.  One branch for all of them: a switch inside
+// the unrolled loops of the epilogues made code of some 100 KB, and fetching
+// it took longer than the product (down projection of 4095 tokens: 326 us).
+template <int NV>
+__device__ __forceinline__ void linear_act(float (&v)[NV], int act) {
+    if (act == K3MOE_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];  // NaN stays NaN
+    } else if (act == K3MOE_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) v[i] = v[i] / (1.0f + expf(-v[i]));
+    } else if (act == K3MOE_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) v[i] = 0.5f * v[i] * erfcf(-0.70710678118654752f * v[i]);
+    } else if (act == K3MOE_ACT_GELU_TANH) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            v[i] = 0.5f * v[i] * (1.0f + tanhf(0.79788456080286536f * (v[i] + 0.044715f * v[i] * v[i] * v[i])));
     }
 }
 
-// One output from its sums: bias, activation, gate and residual in fp32, one
-// rounding.  b, bg: the column's biases; r: the residual.
-__device__ __forceinline__ float linear_value(const LinearParams &p, float v, float g, float b, float bg, float r) {
-    v += b;
-    return (p.wg ? linear_act(g + bg, p.act) * v : linear_act(v, p.act)) + r;
+// NV outputs of one column from their sums, in fp32, before the one rounding:
+// bias, activation, gate and residual.  b, bg: the column's biases.
+template <int NV>
+__device__ __forceinline__ void linear_values(const LinearParams &p, float (&v)[NV], float (&g)[NV], float b, float bg,
+                                              const float (&r)[NV]) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] += b;
+    if (p.wg) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) g[i] += bg;
+        linear_act(g, p.act);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) v[i] *= g[i];
+    } else {
+        linear_act(v, p.act);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] += r[i];
 }
-__device__ __forceinline__ float linear_resid(const LinearParams &p, long long t, int n) {
-    if (!p.resid) return 0.f;
-    return p.out_fp32 ? reinterpret_cast<const float *>(p.resid)[t * p.ldr + n]
-                      : bf16_lo(reinterpret_cast<const uint16_t *>(p.resid)[t * p.ldr + n]);
+// The residuals of NV tokens t, t + step, ... (those past `last` are read as
+// `last`) of column n.  No branch around a single load: its use would have to
+// follow it there, and the loads would wait for one another (4.6 us for 8).
+template <int NV>
+__device__ __forceinline__ void linear_resid(const LinearParams &p, float (&r)[NV], long long t, int step, long long last,
+                                             int n) {
+    if (!p.resid) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) r[i] = 0.f;
+    } else if (p.out_fp32) {
+        const float *q = reinterpret_cast<const float *>(p.resid) + n;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) r[i] = q[min(t + i * step, last) * p.ldr];
+    } else {
+        const uint16_t *q = reinterpret_cast<const uint16_t *>(p.resid) + n;
+        uint16_t h[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) h[i] = q[min(t + i * step, last) * p.ldr];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) r[i] = bf16_lo(h[i]);
+    }
 }
+__device__ __forceinline__ uint16_t bf16_bits(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
 __device__ __forceinline__ void linear_store(const LinearParams &p, long long t, int n, float a) {
     if (p.out_fp32)
         reinterpret_cast<float *>(p.out)[t * p.ldo + n] = a;
     else
-        reinterpret_cast<uint16_t *>(p.out)[t * p.ldo + n] = __bfloat16_as_ushort(__float2bfloat16_rn(a));
+        reinterpret_cast<uint16_t *>(p.out)[t * p.ldo + n] = bf16_bits(a);
 }
 
 // ------------------------------------------------------ few tokens: stream --
@@ -76,49 +116,67 @@ __device__ __forceinline__ uint4 ldg_once(const uint4 *p) {  // no reuse inside 
 }
 
 // RG: groups of 8 weight rows per CTA; TG: 8-token halves; U: 64-wide units
-// whose loads are in flight together.
+// whose loads are in flight together.  Rows and tokens past the last are read
+// as the last one, and their sums dropped.
 template <int RG, bool GATED, int TG, int U>
-__global__ void __launch_bounds__(512) linear_stream_kernel(const __grid_constant__ LinearParams p) {
+__global__ void __launch_bounds__(512, 1) linear_stream_kernel(const __grid_constant__ LinearParams p) {
     constexpr int NM = RG * (GATED ? 2 : 1);
     extern __shared__ float red[];  // [warps][NM][8 * TG tokens][8 rows]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
     const int g = lane >> 2, q = lane & 3;
     const int n0 = blockIdx.x * RG * 8;
-    const int units = ceil_div(p.K, 64);
+    const uint16_t *wr[NM], *xr[TG];
+#pragma unroll
+    for (int r = 0; r < NM; ++r)
+        wr[r] = (GATED && (r & 1) ? p.wg : p.w) + (long long)min(n0 + (GATED ? r >> 1 : r) * 8 + g, p.N - 1) * p.ldw + q * 8;
+#pragma unroll
+    for (int t = 0; t < TG; ++t) xr[t] = p.x + (long long)min(g + 8 * t, p.T - 1) * p.ldx + q * 8;
     pdl_wait();
     pdl_trigger();
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
     float sum[NM][4] = {};
-    for (int u0 = warp; u0 < units; u0 += nw * U) {
-        uint4 w[U][2][NM];
+    auto step = [&](float (&d)[4], const uint4 &xa, const uint4 &xb, const uint4 &w) {
+        mma_16816(d, xa.x, xb.x, xa.y, xb.y, w.x, w.y);
+        mma_16816(d, xa.z, xb.z, xa.w, xb.w, w.z, w.w);
+    };
+    const int units = ceil_div(p.K, 64);
+    for (int u = warp; u < units; u += nw * U) {
+        // units past the last are read as this warp's first and not used; in
+        // the last unit, k past K is read as the row's last 8 and replaced by 0
+        uint4 w[U][2][NM], x[U][2][TG];
+        auto at = [&](int i, int h) { return min((u + i * nw < units ? u + i * nw : u) * 64 + h * 32, p.K - 8 - q * 8); };
 #pragma unroll
         for (int i = 0; i < U; ++i)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int k = (u0 + i * nw) * 64 + h * 32 + q * 8;  // below 2^25
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int r = 0; r < NM; ++r) {
-                    const int n = n0 + (GATED ? r >> 1 : r) * 8 + g;
-                    const uint16_t *row = (GATED && (r & 1) ? p.wg : p.w) + (long long)n * p.ldw;
-                    w[i][h][r] = k < p.K && n < p.N ? ldg_once(reinterpret_cast<const uint4 *>(row + k)) : zero;
-                }
-            }
-        float part[NM][4] = {};  // chains of 4 U steps at most; the rest is added in fp32
+                for (int r = 0; r < NM; ++r) w[i][h][r] = ldg_once(reinterpret_cast<const uint4 *>(wr[r] + at(i, h)));
 #pragma unroll
         for (int i = 0; i < U; ++i)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int k = (u0 + i * nw) * 64 + h * 32 + q * 8;
-                uint4 xa = zero, xb = zero;
-                if (k < p.K && g < p.T) xa = __ldg(reinterpret_cast<const uint4 *>(p.x + g * p.ldx + k));
-                if (TG == 2 && k < p.K && g + 8 < p.T)
-                    xb = __ldg(reinterpret_cast<const uint4 *>(p.x + (g + 8) * p.ldx + k));
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int r = 0; r < NM; ++r) {
-                    mma_16816(part[r], xa.x, xb.x, xa.y, xb.y, w[i][h][r].x, w[i][h][r].y);
-                    mma_16816(part[r], xa.z, xb.z, xa.w, xb.w, w[i][h][r].z, w[i][h][r].w);
-                }
+                for (int t = 0; t < TG; ++t) x[i][h][t] = __ldg(reinterpret_cast<const uint4 *>(xr[t] + at(i, h)));
+        float part[NM][4] = {};  // chains of 4 U steps; the rest is added in fp32
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int k = (u + i * nw) * 64;
+            if (u + i * nw >= units) break;
+            if (k + 64 > p.K) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (k + h * 32 + q * 8 >= p.K) {
+#pragma unroll
+                        for (int r = 0; r < NM; ++r) w[i][h][r] = zero;
+#pragma unroll
+                        for (int t = 0; t < TG; ++t) x[i][h][t] = zero;
+                    }
             }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int r = 0; r < NM; ++r) step(part[r], x[i][h][0], TG == 2 ? x[i][h][TG - 1] : zero, w[i][h][r]);
+        }
 #pragma unroll
         for (int r = 0; r < NM; ++r)
 #pragma unroll
@@ -136,14 +194,17 @@ __global__ void __launch_bounds__(512) linear_stream_kernel(const __grid_constan
         const int rg = i / (TT * 8), t = (i / 8) % TT, n = n0 + rg * 8 + i % 8;
         if (t >= p.T || n >= p.N) continue;
         const float b = p.bias ? __ldg(p.bias + n) : 0.f, bg = p.bias_g ? __ldg(p.bias_g + n) : 0.f;
-        const float res = linear_resid(p, t, n);
-        float v = 0.f, gv = 0.f;
+        float res[1];
+        linear_resid(p, res, t, 0, t, n);
+        float v[1] = {0.f}, gv[1] = {0.f};
         const float *src = red + (GATED ? 2 * rg : rg) * TT * 8 + i % (TT * 8);
+#pragma unroll 4
         for (int w = 0; w < nw; ++w) {
-            v += src[w * NM * TT * 8];
-            if (GATED) gv += src[(w * NM + 1) * TT * 8];
+            v[0] += src[w * NM * TT * 8];
+            if (GATED) gv[0] += src[(w * NM + 1) * TT * 8];
         }
-        linear_store(p, t, n, linear_value(p, v, gv, b, bg, res));
+        linear_values(p, v, gv, b, bg, res);
+        linear_store(p, t, n, v[0]);
     }
 }
 
@@ -159,7 +220,7 @@ constexpr int kLtA = 128 * 128;  // bytes of the weight box per stage
 constexpr int kLtHead = 1024;    // barriers, before the stages
 constexpr int kLtMaxStages = 10;
 constexpr int kLtMaxSplit = 8;
-constexpr int kLtChain = 4;      // K-steps per accumulation chain of an fp32 output
+constexpr int kLtChain = 8;      // K-steps per accumulation chain of an fp32 output
 constexpr int kLinearMaxT = 1 << 30;
 
 struct LinearTcParams {
@@ -186,13 +247,10 @@ __device__ __forceinline__ void prefetch_tmap(const void *m) { asm volatile("pre
 // own columns, adding the parts in rank order.
 //
 // The tensor core cuts its running sum at every step, so a long chain drifts:
-// with fp32 outputs the sum moves to registers every `chain` K-steps (two
+// with fp32 outputs the sum moves to shared memory every `chain` K-steps (two
 // tensor-memory buffers) and the pieces are added there, rounded to nearest;
 // bf16 outputs take one chain, whose drift (2^-24 a step of 16) is far below
 // the output's half step of 2^-9.
-//
-// NC: 16-column pieces per epilogue warp (bn <= 32 NC).
-template <int NC>
 __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid_constant__ LinearTcParams a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -208,7 +266,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
     volatile int *s_abort = reinterpret_cast<volatile int *>(tslot + 1);
     uint8_t *stages = smem + kLtHead;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (S > 1) umma::cluster_arrive();  // "this CTA has started": waited for before the first remote write
+    if (S > 1) umma::cluster_arrive();  // "this CTA has started": a remote write needs it
     if (threadIdx.x == 0) {
         for (int s = 0; s < nst; ++s) {
             mbar_init(&full[s], 1);
@@ -229,6 +287,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
     if (warp == 0) umma::tmem_alloc(tslot, (uint32_t)a.tcols);
     umma::fence_before();
     __syncthreads();
+    if (S > 1) umma::cluster_wait();
     umma::fence_after();
     const uint32_t tbase = *tslot;
     const int rank = S > 1 ? (int)umma::cluster_rank() : 0;
@@ -239,24 +298,23 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
     const int nkt = ceil_div(p.K, kLtKStep);
     const int kt0 = (int)((long long)nkt * rank / S), nk = (int)((long long)nkt * (rank + 1) / S) - kt0;
     const int nch = ceil_div(nk, a.chain);
-    auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (*s_abort) return false;
-        if (mbar_wait_bounded(bar, parity, a.hdr, a.wait_ns)) return true;
-        *s_abort = 1;
-        return false;
-    };
+    const int cpo = ceil_div(bn, S);  // columns that one CTA of the cluster finishes
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait_warp(bar, parity, a.hdr, a.wait_ns, s_abort); };
     pdl_wait();
     pdl_trigger();
 
     const int half = warp >> 2, hcols = ((bn / 16 + 1) / 2) * 16;  // columns of the first of a quadrant's warps
     const int c0 = half * hcols, ncol = half ? bn - hcols : hcols;
-    float acc[NC][16];
+    // red[source][column][row]: the columns this CTA finishes; sum[column][row]:
+    // this CTA's sums of the chains before the last (one CTA: the same buffer)
+    float *red = reinterpret_cast<float *>(smem + a.red);
+    float *sum = S > 1 ? red + S * cpo * 128 : red;
     if (warp == 8) {
-        if (lane == 0) {
-            int i = 0;
-            for (; i < nk; ++i) {
-                const int s = i % nst;
-                if (i >= nst && !wait(&empty[s], (uint32_t)(((i / nst) + 1) & 1))) break;
+        int i = 0, s = 0;
+        uint32_t ph = 1u;  // of the empty barriers: the first round's waits pass at once
+        for (; i < nk; ++i) {
+            if (!wait(&empty[s], ph)) break;
+            if (umma::elect()) {
                 uint8_t *st = stages + s * SB;
                 const int x = (kt0 + i) * kLtKStep;
                 mbar_arrive_expect_tx(&full[s], (uint32_t)SB);
@@ -264,65 +322,90 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
                 if (gated) umma::tma_load_2d(st + kLtA / 2, a.twg, x, n0, &full[s]);
                 umma::tma_load_2d(st + kLtA, a.tx, x, t0, &full[s]);
             }
-            if (*s_abort) {
-                for (int s = 0; s < nst && s < i; ++s) {
-                    const int last = s + ((i - 1 - s) / nst) * nst;
-                    mbar_drain(&full[s], (uint32_t)((last / nst) & 1), a.wait_ns);
-                }
+            __syncwarp();
+            if (++s == nst) {
+                s = 0;
+                ph ^= 1u;
+            }
+        }
+        if (*s_abort && lane == 0) {
+            for (int t = 0; t < nst && t < i; ++t) {
+                const int last = t + ((i - 1 - t) / nst) * nst;
+                mbar_drain(&full[t], (uint32_t)((last / nst) & 1), a.wait_ns);
             }
         }
     } else if (warp == 9) {
-        if (lane == 0) {
-            const uint64_t adesc = umma::smem_desc(smem_u32(stages), 16u, 1024u, umma::kLayoutSw128);
-            const uint32_t idesc = umma::idesc_bf16(bn);
-            bool ok = true;
-            for (int c = 0; c < nch && ok; ++c) {
-                const int buf = c & 1;
-                if (c >= 2 && !wait(&aempty[buf], (uint32_t)(((c >> 1) + 1) & 1))) break;
-                umma::fence_after();
-                const uint32_t d = tbase + (uint32_t)(buf * bn);
-                uint32_t go = 0u;
-                const int i1 = min(nk, (c + 1) * a.chain);
-                for (int i = c * a.chain; i < i1; ++i) {
-                    const int s = i % nst;
-                    if (!wait(&full[s], (uint32_t)((i / nst) & 1))) {
-                        ok = false;
-                        break;
-                    }
-                    umma::fence_after();
-                    const uint64_t ad = adesc + ((uint32_t)(s * SB) >> 4), bd = ad + (kLtA >> 4);
-                    const int steps = min(4, ceil_div(p.K - (kt0 + i) * kLtKStep, 16));  // past K: zeros from TMA
-#pragma unroll
-                    for (int sk = 0; sk < 4; ++sk) {
-                        if (sk < steps) {
-                            umma::mma_bf16(d, ad + 2 * sk, bd + 2 * sk, idesc, go);
-                            go = 1u;
-                        }
-                    }
-                    umma::commit(&empty[s]);
+        const uint64_t adesc = umma::smem_desc(smem_u32(stages), 16u, 1024u, umma::kLayoutSw128);
+        const uint32_t idesc = umma::idesc_bf16(bn);
+        int i = 0, s = 0;
+        uint32_t ph = 0u;
+        bool ok = true;
+        for (int c = 0; c < nch && ok; ++c) {
+            const int buf = c & 1;
+            if (c >= 2 && !wait(&aempty[buf], (uint32_t)(((c >> 1) + 1) & 1))) break;
+            const uint32_t d = tbase + (uint32_t)(buf * bn);
+            const int i0 = i, i1 = min(nk, i + a.chain);
+            for (; i < i1; ++i) {
+                if (!wait(&full[s], ph)) {
+                    ok = false;
+                    break;
                 }
-                umma::commit(&afull[buf]);
+                umma::fence_after();
+                const uint64_t ad = adesc + ((uint32_t)(s * SB) >> 4), bd = ad + (kLtA >> 4);
+                const int steps = ceil_div(p.K - (kt0 + i) * kLtKStep, 16);  // past K: zeros from TMA
+                if (umma::elect()) {
+                    umma::mma_bf16(d, ad, bd, idesc, i > i0 ? 1u : 0u);
+                    if (steps > 1) umma::mma_bf16(d, ad + 2, bd + 2, idesc, 1u);
+                    if (steps > 2) umma::mma_bf16(d, ad + 4, bd + 4, idesc, 1u);
+                    if (steps > 3) umma::mma_bf16(d, ad + 6, bd + 6, idesc, 1u);
+                    umma::commit(&empty[s]);
+                    if (i + 1 == i1) umma::commit(&afull[buf]);
+                }
+                __syncwarp();
+                if (++s == nst) {
+                    s = 0;
+                    ph ^= 1u;
+                }
             }
+        }
+        if (umma::elect()) {
             umma::commit(mdone);
             mbar_drain(mdone, 0u, a.wait_ns);
         }
     } else {
         for (int c = 0; c < nch; ++c) {
             const int buf = c & 1;
-            int got = 0;
-            if (lane == 0) got = wait(&afull[buf], (uint32_t)((c >> 1) & 1));
-            if (!__shfl_sync(0xffffffffu, got, 0)) break;
+            if (!wait(&afull[buf], (uint32_t)((c >> 1) & 1))) break;
             umma::fence_after();
             const uint32_t src = tbase + umma::lane_base(warp) + (uint32_t)(buf * bn + c0);
+            const bool last = c == nch - 1;
+            int o = c0 / cpo, jo = c0 - o * cpo;  // where column c0 goes: CTA o's column jo
+            const int row = 32 * (warp & 3) + lane, cend = min(c0 + ncol, p.T - t0);
+            const uint32_t mine = smem_u32(red) + (uint32_t)(rank * cpo * 128 + row) * 4u;
+            for (int j = c0; j < cend; j += 16) {
+                uint32_t r[16];
+                float v[16];
+                umma::ld16(src + (j - c0), r);
+                umma::wait_ld();
+                float *sj = sum + j * 128 + row;
 #pragma unroll
-            for (int j = 0; j < NC; ++j) {
-                if (16 * j < ncol) {
-                    uint32_t r[16];
-                    umma::ld16(src + 16 * j, r);
-                    umma::wait_ld();
+                for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+                if (c > 0) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        acc[j][i] = c == 0 ? __uint_as_float(r[i]) : acc[j][i] + __uint_as_float(r[i]);
+                    for (int i = 0; i < 16; ++i) v[i] += sj[i * 128];
+                }
+                if (!last || S == 1) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) sj[i * 128] = v[i];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        if (j + i < cend) umma::st_cluster(umma::mapa(mine + (uint32_t)jo * 512u, (uint32_t)o), v[i]);
+                        if (++jo == cpo) {
+                            jo = 0;
+                            ++o;
+                        }
+                    }
                 }
             }
             umma::fence_before();
@@ -333,74 +416,37 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
     }
     __syncwarp();
 
-    const int row = 32 * (warp & 3) + lane;
-    if (S == 1 && !gated) {
-        const int n = n0 + row;
-        if (warp < 8 && n < p.N) {
-            const float b = p.bias ? __ldg(p.bias + n) : 0.f;
-#pragma unroll
-            for (int j = 0; j < NC; ++j) {
-                if (16 * j < ncol) {
-                    float r[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const long long t = (long long)t0 + c0 + 16 * j + i;
-                        r[i] = t < p.T ? linear_resid(p, t, n) : 0.f;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const long long t = (long long)t0 + c0 + 16 * j + i;
-                        if (t < p.T) linear_store(p, t, n, linear_value(p, acc[j][i], 0.f, b, 0.f, r[i]));
-                    }
-                }
-            }
-        }
+    if (S > 1) {
+        umma::cluster_arrive();
+        umma::cluster_wait();
     } else {
-        // red[source][column][row] of the columns this CTA finishes
-        const int cpo = ceil_div(bn, S);
-        float *red = reinterpret_cast<float *>(smem + a.red);
-        if (S > 1) umma::cluster_wait();
-        if (warp < 8) {
-            const uint32_t base = smem_u32(red) + (uint32_t)(rank * cpo * 128 + row) * 4u;
+        __syncthreads();
+    }
+    const int nl = threadIdx.x & (nrow - 1), n = n0 + nl, step = 256 / nrow;
+    if (warp < 8 && n < p.N) {
+        constexpr int NV = 8;  // columns whose residuals are fetched together
+        const int jmax = min(cpo, min(bn, p.T - t0) - rank * cpo);
+        const float b = p.bias ? __ldg(p.bias + n) : 0.f;
+        const float bg = p.bias_g ? __ldg(p.bias_g + n) : 0.f;
+        for (int j0 = threadIdx.x / nrow; j0 < jmax; j0 += NV * step) {
+            const long long t = (long long)t0 + rank * cpo + j0;
+            float v[NV], g[NV], res[NV];
+            linear_resid(p, res, t, step, (long long)t0 + rank * cpo + jmax - 1, n);
 #pragma unroll
-            for (int j = 0; j < NC; ++j) {
-                if (16 * j < ncol) {
+            for (int i = 0; i < NV; ++i) v[i] = g[i] = 0.f;
+            const float *r = red + nl;
+            for (int s = 0; s < S; ++s, r += cpo * 128) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int col = c0 + 16 * j + i, o = col / cpo;
-                        if (t0 + col < p.T) {
-                            const uint32_t at = base + (uint32_t)(col - o * cpo) * 512u;
-                            umma::st_cluster(S > 1 ? umma::mapa(at, (uint32_t)o) : at, acc[j][i]);
-                        }
-                    }
+                for (int i = 0; i < NV; ++i) {
+                    const int j = min(j0 + i * step, jmax - 1);
+                    v[i] += r[j * 128];
+                    if (gated) g[i] += r[j * 128 + 64];
                 }
             }
-        }
-        if (S > 1) {
-            umma::cluster_arrive();
-            umma::cluster_wait();
-        } else {
-            __syncthreads();
-        }
-        if (warp < 8) {
-            const int nl = threadIdx.x & (nrow - 1), n = n0 + nl, step = 256 / nrow;
-            const int jmax = min(cpo, min(bn, p.T - t0) - rank * cpo);
-            const float b = p.bias && n < p.N ? __ldg(p.bias + n) : 0.f;
-            const float bg = p.bias_g && n < p.N ? __ldg(p.bias_g + n) : 0.f;
-            if (n < p.N) {
-#pragma unroll 4
-                for (int j = threadIdx.x / nrow; j < jmax; j += step) {
-                    const long long t = (long long)t0 + rank * cpo + j;
-                    const float res = linear_resid(p, t, n);
-                    const float *r = red + j * 128 + nl;
-                    float v = 0.f, g = 0.f;
-                    for (int s = 0; s < S; ++s) {
-                        v += r[s * cpo * 128];
-                        if (gated) g += r[s * cpo * 128 + 64];
-                    }
-                    linear_store(p, t, n, linear_value(p, v, g, b, bg, res));
-                }
-            }
+            linear_values(p, v, g, b, bg, res);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (j0 + i * step < jmax) linear_store(p, t + i * step, n, v[i]);
         }
     }
     umma::fence_before();
@@ -471,79 +517,87 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_pair_kernel(const __grid
         n0 = ((in / w) * 2 + rank) * nrow;
         t0 = (band * 8 + in % w) * bn;
     };
-    auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (*s_abort) return false;
-        if (mbar_wait_bounded(bar, parity, a.hdr, a.wait_ns)) return true;
-        *s_abort = 1;
-        return false;
-    };
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait_warp(bar, parity, a.hdr, a.wait_ns, s_abort); };
     pdl_wait();
     pdl_trigger();
 
     if (warp == 8) {
-        if (lane == 0) {
-            int i = 0;
-            for (int it = pair; it < items && !*s_abort; it += pairs) {
-                int n0, t0;
-                tile_at(it, n0, t0);
-                for (int kt = 0; kt < nk; ++kt, ++i) {
-                    const int s = i % nst;
-                    if (i >= nst && !wait(&empty[s], (uint32_t)(((i / nst) + 1) & 1))) break;
+        int i = 0, s = 0;
+        uint32_t ph = 1u;
+        bool ok = true;
+        for (int it = pair; it < items && ok; it += pairs) {
+            int n0, t0;
+            tile_at(it, n0, t0);
+            const int tx = t0 + rank * (bn / 2);
+            for (int kt = 0; kt < nk; ++kt, ++i) {
+                if (!wait(&empty[s], ph)) {
+                    ok = false;
+                    break;
+                }
+                if (umma::elect()) {
                     uint8_t *st = stages + s * SB;
                     const uint32_t bar = umma::mapa(smem_u32(&full[s]), 0u);
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)(2 * SB));
                     umma::tma_load_2d_pair(st, a.tw, kt * kLtKStep, n0, bar);
                     if (gated) umma::tma_load_2d_pair(st + kLtA / 2, a.twg, kt * kLtKStep, n0, bar);
-                    umma::tma_load_2d_pair(st + kLtA, a.tx, kt * kLtKStep, t0 + rank * (bn / 2), bar);
+                    umma::tma_load_2d_pair(st + kLtA, a.tx, kt * kLtKStep, tx, bar);
                 }
-            }
-            if (*s_abort && rank == 0) {
-                for (int s = 0; s < nst && s < i; ++s) {
-                    const int last = s + ((i - 1 - s) / nst) * nst;
-                    mbar_drain(&full[s], (uint32_t)((last / nst) & 1), a.wait_ns);
+                __syncwarp();
+                if (++s == nst) {
+                    s = 0;
+                    ph ^= 1u;
                 }
             }
         }
+        if (*s_abort && rank == 0 && lane == 0) {
+            for (int t = 0; t < nst && t < i; ++t) {
+                const int last = t + ((i - 1 - t) / nst) * nst;
+                mbar_drain(&full[t], (uint32_t)((last / nst) & 1), a.wait_ns);
+            }
+        }
     } else if (warp == 9) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             const uint64_t adesc = umma::smem_desc(smem_u32(stages), 16u, 1024u, umma::kLayoutSw128);
             const uint32_t idesc = umma::idesc_bf16_pair(bn);
-            int i = 0, q = 0;
+            int s = 0, q = 0;
+            uint32_t ph = 0u;
             bool ok = true;
             for (int it = pair; it < items && ok; it += pairs, ++q) {
                 const int buf = q & 1;
                 if (q >= 2 && !wait(&aempty[buf], (uint32_t)(((q >> 1) + 1) & 1))) break;
-                umma::fence_after();
                 const uint32_t d = tbase + (uint32_t)(buf * 256);
-                uint32_t go = 0u;
-                for (int kt = 0; kt < nk; ++kt, ++i) {
-                    const int s = i % nst;
-                    if (!wait(&full[s], (uint32_t)((i / nst) & 1))) {
+                for (int kt = 0; kt < nk; ++kt) {
+                    if (!wait(&full[s], ph)) {
                         ok = false;
                         break;
                     }
                     umma::fence_after();
                     const uint64_t ad = adesc + ((uint32_t)(s * SB) >> 4), bd = ad + (kLtA >> 4);
-                    const int steps = min(4, ceil_div(p.K - kt * kLtKStep, 16));
-#pragma unroll
-                    for (int sk = 0; sk < 4; ++sk) {
-                        if (sk < steps) {
-                            umma::mma_bf16_pair(d, ad + 2 * sk, bd + 2 * sk, idesc, go);
-                            go = 1u;
-                        }
+                    const int steps = ceil_div(p.K - kt * kLtKStep, 16);
+                    if (umma::elect()) {
+                        umma::mma_bf16_pair(d, ad, bd, idesc, kt > 0 ? 1u : 0u);
+                        if (steps > 1) umma::mma_bf16_pair(d, ad + 2, bd + 2, idesc, 1u);
+                        if (steps > 2) umma::mma_bf16_pair(d, ad + 4, bd + 4, idesc, 1u);
+                        if (steps > 3) umma::mma_bf16_pair(d, ad + 6, bd + 6, idesc, 1u);
+                        umma::commit_pair(&empty[s]);
+                        if (kt + 1 == nk) umma::commit_pair(&afull[buf]);
                     }
-                    umma::commit_pair(&empty[s]);
+                    __syncwarp();
+                    if (++s == nst) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
                 }
-                umma::commit_pair(&afull[buf]);
             }
-            umma::commit_pair(mdone);
+            if (umma::elect()) umma::commit_pair(mdone);
+            __syncwarp();
         }
-        if (lane == 0) mbar_drain(mdone, 0u, a.wait_ns);  // in both CTAs: the last arrival from the pair's MMAs
+        wait(mdone, 0u);  // in both CTAs: the last arrival from the pair's MMAs
     } else {
         // Epilogue: warp w takes lane quadrant w % 4 and every second group of
-        // 32 tokens.  Gated: quadrants 0, 1 hold w's rows and 2, 3 w_gate's;
-        // the warps of quadrants u and u + 2 exchange halves, so that one
-        // finishes 16 of the 32 tokens and the other the rest.
+        // 16 tokens.  Gated: quadrants 0, 1 hold w's rows and 2, 3 w_gate's;
+        // the warps of quadrants u and u + 2 take groups of 32 and exchange
+        // halves, so that one finishes 16 of the tokens and the other the rest.
         const int quad = warp & 3, hv = warp >> 2;
         float *ex = reinterpret_cast<float *>(stages + nst * SB) + ((quad & 1) * 2 + hv) * (32 * 32);
         const int nl = gated ? 32 * (quad & 1) + lane : 32 * quad + lane;
@@ -555,52 +609,58 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_pair_kernel(const __grid
             const bool nin = n < p.N;
             const float b = p.bias && nin ? __ldg(p.bias + n) : 0.f;
             const float bg = p.bias_g && nin ? __ldg(p.bias_g + n) : 0.f;
-            const uint16_t *rp = reinterpret_cast<const uint16_t *>(p.resid);
-            uint16_t *op = reinterpret_cast<uint16_t *>(p.out);
-            int got = 0;
-            if (lane == 0) got = wait(&afull[buf], (uint32_t)((q >> 1) & 1));
-            got = __shfl_sync(0xffffffffu, got, 0);
+            const int left = nin ? p.T - t0 : 0;  // tokens of this tile to store
+            const uint16_t *rp = reinterpret_cast<const uint16_t *>(p.resid) + (long long)t0 * p.ldr + n;
+            uint16_t *op = reinterpret_cast<uint16_t *>(p.out) + (long long)t0 * p.ldo + n;
+            // The residuals of the 16 tokens from f on, loaded one group ahead
+            // of their use (the first while the tile's MMAs run).
+            uint16_t rn[16] = {};
+            auto fetch = [&](int f) {
+                if (p.resid && f < bn && left > 0) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) rn[j] = rp[(long long)min(f + j, left - 1) * p.ldr];
+                }
+            };
+            const bool low = quad < 2;  // gated: holds w's sums
+            const int gstep = gated ? 64 : 32, f0 = gated ? hv * 32 + (low ? 0 : 16) : hv * 16;
+            fetch(f0);
+            bool got = wait(&afull[buf], (uint32_t)((q >> 1) & 1));
             // the two warps that exchange go on together or not at all
-            if (gated) got = umma::bar_red_and(1 + (quad & 1) * 2 + hv, 64, got != 0);
+            if (gated) got = umma::bar_red_and(1 + (quad & 1) * 2 + hv, 64, got);
             if (!got) break;
             umma::fence_after();
             const uint32_t src = tbase + umma::lane_base(warp) + (uint32_t)(buf * 256);
-            for (int c = hv * 32; c < bn; c += 64) {
-                uint32_t v[32];
-                umma::ld32(src + c, v);
-                const int tc = t0 + c;
-                if (!gated) {
-                    uint32_t r[32];
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        r[j] = rp && nin && tc + j < p.T ? rp[(long long)(tc + j) * p.ldr + n] : 0u;
+            for (int f = f0; f < bn; f += gstep) {  // the 16 tokens this warp finishes
+                float v[16], g[16], r[16];
+                uint32_t raw[16];
+                umma::ld16(src + f, raw);
+                if (gated) {
+                    uint32_t give[16];
+                    umma::ld16(src + (low ? f + 16 : f - 16), give);
                     umma::wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (nin && tc + j < p.T)
-                            op[(long long)(tc + j) * p.ldo + n] = __bfloat16_as_ushort(__float2bfloat16_rn(
-                                linear_act(__uint_as_float(v[j]) + b, p.act) + bf16_lo(r[j])));
-                } else {
-                    umma::wait_ld();
-                    const bool low = quad < 2;  // holds w's sums, finishes tokens 0-15
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        ex[(low ? j + 16 : j) * 32 + lane] = __uint_as_float(low ? v[j + 16] : v[j]);
-                    }
-                    umma::bar_sync(1 + (quad & 1) * 2 + hv, 64);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float other = ex[(low ? j : j + 16) * 32 + lane];
-                        const float mine = __uint_as_float(low ? v[j] : v[j + 16]);
-                        const int t = tc + (low ? j : j + 16);
-                        if (nin && t < p.T) {
-                            const float res = rp ? bf16_lo(rp[(long long)t * p.ldr + n]) : 0.f;
-                            const float o = linear_value(p, low ? mine : other, low ? other : mine, b, bg, res);
-                            op[(long long)t * p.ldo + n] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
-                        }
-                    }
+                    for (int j = 0; j < 16; ++j) ex[((low ? 16 : 0) + j) * 32 + lane] = __uint_as_float(give[j]);
                     umma::bar_sync(1 + (quad & 1) * 2 + hv, 64);
                 }
+                umma::wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float mine = __uint_as_float(raw[j]);
+                    v[j] = mine;
+                    if (gated) {
+                        const float other = ex[((low ? 0 : 16) + j) * 32 + lane];
+                        v[j] = low ? mine : other;
+                        g[j] = low ? other : mine;
+                    }
+                    r[j] = bf16_lo(rn[j]);
+                }
+                fetch(f + gstep);
+                linear_values(p, v, g, b, bg, r);
+                uint16_t *o = op + (long long)f * p.ldo;
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (f + j < left) o[j * p.ldo] = bf16_bits(v[j]);
+                if (gated) umma::bar_sync(1 + (quad & 1) * 2 + hv, 64);
             }
             umma::fence_before();
             __syncwarp();

@@ -124,6 +124,16 @@ __device__ __forceinline__ void st4(uint32_t taddr, uint32_t a, uint32_t b, uint
 }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// One lane of a converged warp, the same one every time.  Issue loops run
+// warp-uniform and branch on this only around the issuing instructions, so
+// that descriptors and addresses stay in uniform registers: a loop inside an
+// `if (lane == 0)` took 90 cycles per MMA, most of them moving operands.
+__device__ __forceinline__ bool elect() {
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(ok));
+    return ok != 0;
+}
+
 // Lane-quadrant field of a TMEM address for warp w (lanes 32(w%4)..).
 __device__ __forceinline__ uint32_t lane_base(int warp) { return (uint32_t)(32 * (warp & 3)) << 16; }
 
