@@ -72,13 +72,13 @@ cudaError_t set_smem(Kern kernel, int bytes) {
 }
 
 
-// Clusters of n CTAs (kLtThreads threads, all of an SM's shared memory each)
+// Clusters of n CTAs (of `threads` threads, all of an SM's shared memory each)
 // that the device runs at the same time.
 template <typename Kern>
-cudaError_t max_clusters(Kern kernel, int n, int *out) {
+cudaError_t max_clusters(Kern kernel, int n, int threads, int *out) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(n);
-    cfg.blockDim = dim3(kLtThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = kSmemLimit;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -109,10 +109,13 @@ k3moe_status device_info(DeviceInfo **out) {
         if (r == cudaSuccess) r = set_smem(layer_kernel<0, false>, big);
         if (r == cudaSuccess) r = set_smem(pf_router_mma_kernel, rm_smem_bytes());
         if (r == cudaSuccess) r = set_smem(linear_tile_kernel, big);
-        if (r == cudaSuccess) r = set_smem(linear_pair_kernel, big);
+        if (r == cudaSuccess) r = set_smem(linear_pair_kernel<false, false>, big);
+        if (r == cudaSuccess) r = set_smem(linear_pair_kernel<false, true>, big);
+        if (r == cudaSuccess) r = set_smem(linear_pair_kernel<true, false>, big);
+        if (r == cudaSuccess) r = set_smem(linear_pair_kernel<true, true>, big);
         for (int s = 2; s <= kLtMaxSplit && r == cudaSuccess; ++s)
-            r = max_clusters(linear_tile_kernel, s, &di.clusters[s]);
-        if (r == cudaSuccess) r = max_clusters(linear_pair_kernel, 2, &di.pairs);
+            r = max_clusters(linear_tile_kernel, s, kLtThreads, &di.clusters[s]);
+        if (r == cudaSuccess) r = max_clusters(linear_pair_kernel<true, true>, 2, kLpThreads, &di.pairs);
         if (r != cudaSuccess) return cuda_fail(r);
         di.ready = true;
     }
@@ -936,10 +939,13 @@ k3moe_status linear_launch(const LinearParams &p, WsHeader *hdr, cudaStream_t st
     if (s != K3MOE_OK) return s;
     const int room = kSmemLimit - 1024 - kLtHead;
     if (pair) {
-        const int sb = kLtA + a.bn * 64, ex = gated ? kLpExch : 0;
-        a.nst = std::min((room - ex) / sb, kLtMaxStages);
+        const int sb = kLtA + a.bn * 64;
+        a.nst = std::min((room - kLpExch) / sb, kLtMaxStages);
         const int pairs = (int)std::min<long long>(di->pairs, (long long)a.nrb * a.ntt);
-        e = launch_cluster(linear_pair_kernel, 2 * pairs, kLtThreads, 1024 + kLtHead + a.nst * sb + ex, 2, st, a);
+        const size_t bytes = 1024 + kLtHead + a.nst * sb + kLpExch;
+        auto kernel = gated ? (p.resid ? linear_pair_kernel<true, true> : linear_pair_kernel<true, false>)
+                            : (p.resid ? linear_pair_kernel<false, true> : linear_pair_kernel<false, false>);
+        e = launch_cluster(kernel, 2 * pairs, kLpThreads, bytes, 2, st, a);
         return e == cudaSuccess ? K3MOE_OK : cuda_fail(e, "linear launch");
     }
     const int sb = kLtA + a.bn * 128;
@@ -1419,6 +1425,7 @@ k3moe_status k3moe_linear(const void *x, int64_t ldx, int32_t T, const void *w, 
     p.K = k;
     p.act = lin->act;
     p.out_fp32 = out32;
+    p.vec = aligned(out, 16) && ldo * osz % 16 == 0 && (!residual || (aligned(residual, 16) && ldr * osz % 16 == 0));
     return linear_launch(p, reinterpret_cast<WsHeader *>(ws), reinterpret_cast<cudaStream_t>(stream));
 }
 

@@ -16,6 +16,7 @@ struct LinearParams {
     void *out;                 // T rows, ldo elements apart
     long long ldx, ldw, ldr, ldo;
     int T, N, K, act, out_fp32;
+    int vec;                   // out's and resid's rows are 16-byte aligned
 };
 
 // The activation of NV values.  One branch for all of them: a switch inside
@@ -39,53 +40,107 @@ __device__ __forceinline__ void linear_act(float (&v)[NV], int act) {
     }
 }
 
-// NV outputs of one column from their sums, in fp32, before the one rounding:
-// bias, activation, gate and residual.  b, bg: the column's biases.
+__device__ __forceinline__ uint16_t bf16_bits(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
+
+// The epilogues finish NV neighbouring columns of one token in a thread: one
+// 16-byte access to the residual and to the output (bf16, NV = 8) where their
+// rows allow it.  (One column per lane, 2-byte accesses: the down projection
+// of 4095 tokens took 114 us.)
 template <int NV>
-__device__ __forceinline__ void linear_values(const LinearParams &p, float (&v)[NV], float (&g)[NV], float b, float bg,
-                                              const float (&r)[NV]) {
+struct Residual {
+    uint32_t w[NV];  // fp32 bits, or NV bf16 in the first half
+};
+
+// Loads only: nothing here waits for them.
+template <int NV>
+__device__ __forceinline__ void linear_resid(const LinearParams &p, long long t, int n, Residual<NV> &r, bool out_fp32) {
+    if (!p.resid) return;
+    if (out_fp32) {
+        const float *q = reinterpret_cast<const float *>(p.resid) + t * p.ldr + n;
+        if (NV % 4 == 0 && p.vec && n + NV <= p.N) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] += b;
-    if (p.wg) {
+            for (int i = 0; i < NV; i += 4) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(q + i);
+                r.w[i] = v.x, r.w[i + 1] = v.y, r.w[i + 2] = v.z, r.w[i + 3] = v.w;
+            }
+        } else {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) g[i] += bg;
+            for (int i = 0; i < NV; ++i) r.w[i] = __float_as_uint(q[min(i, p.N - 1 - n)]);
+        }
+    } else {
+        const uint16_t *q = reinterpret_cast<const uint16_t *>(p.resid) + t * p.ldr + n;
+        if (NV == 8 && p.vec && n + NV <= p.N) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(q);
+            r.w[0] = v.x, r.w[1 % NV] = v.y, r.w[2 % NV] = v.z, r.w[3 % NV] = v.w;
+        } else {
+            uint16_t h[NV];
+#pragma unroll
+            for (int i = 0; i < NV; ++i) h[i] = q[min(i, p.N - 1 - n)];
+#pragma unroll
+            for (int i = 0; i < NV; i += 2) r.w[i / 2] = h[i] | (uint32_t)(NV > 1 ? h[(i + 1) % NV] : 0) << 16;
+        }
+    }
+}
+
+// v, g: the sums; b, bg: the columns' biases.  Bias, activation, gate and
+// residual in fp32, one rounding.
+template <int NV>
+__device__ __forceinline__ void linear_finish(const LinearParams &p, long long t, int n, float (&v)[NV], float (&g)[NV],
+                                              const float (&b)[NV], const float (&bg)[NV], const Residual<NV> &r,
+                                              bool gated, bool resid, bool out_fp32) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] += b[i];
+    if (gated) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) g[i] += bg[i];
         linear_act(g, p.act);
 #pragma unroll
         for (int i = 0; i < NV; ++i) v[i] *= g[i];
     } else {
         linear_act(v, p.act);
     }
+    if (resid) {
+        if (out_fp32) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] += r[i];
-}
-// The residuals of NV tokens t, t + step, ... (those past `last` are read as
-// `last`) of column n.  No branch around a single load: its use would have to
-// follow it there, and the loads would wait for one another (4.6 us for 8).
-template <int NV>
-__device__ __forceinline__ void linear_resid(const LinearParams &p, float (&r)[NV], long long t, int step, long long last,
-                                             int n) {
-    if (!p.resid) {
+            for (int i = 0; i < NV; ++i) v[i] += __uint_as_float(r.w[i]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) r[i] = 0.f;
-    } else if (p.out_fp32) {
-        const float *q = reinterpret_cast<const float *>(p.resid) + n;
+            for (int i = 0; i < NV; ++i) v[i] += i % 2 ? bf16_hi(r.w[i / 2]) : bf16_lo(r.w[i / 2]);
+        }
+    }
+    if (out_fp32) {
+        float *q = reinterpret_cast<float *>(p.out) + t * p.ldo + n;
+        if (NV % 4 == 0 && p.vec && n + NV <= p.N) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) r[i] = q[min(t + i * step, last) * p.ldr];
+            for (int i = 0; i < NV; i += 4)
+                *reinterpret_cast<float4 *>(q + i) = make_float4(v[i], v[(i + 1) % NV], v[(i + 2) % NV], v[(i + 3) % NV]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (n + i < p.N) q[i] = v[i];
+        }
     } else {
-        const uint16_t *q = reinterpret_cast<const uint16_t *>(p.resid) + n;
+        uint16_t *q = reinterpret_cast<uint16_t *>(p.out) + t * p.ldo + n;
         uint16_t h[NV];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) h[i] = q[min(t + i * step, last) * p.ldr];
+        for (int i = 0; i < NV; ++i) h[i] = bf16_bits(v[i]);
+        if (NV == 8 && p.vec && n + NV <= p.N) {
+            uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) r[i] = bf16_lo(h[i]);
+            for (int i = 0; i < 4; ++i) w[i] = h[2 * i % NV] | (uint32_t)h[(2 * i + 1) % NV] << 16;
+            *reinterpret_cast<uint4 *>(q) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (n + i < p.N) q[i] = h[i];
+        }
     }
 }
-__device__ __forceinline__ uint16_t bf16_bits(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
-__device__ __forceinline__ void linear_store(const LinearParams &p, long long t, int n, float a) {
-    if (p.out_fp32)
-        reinterpret_cast<float *>(p.out)[t * p.ldo + n] = a;
-    else
-        reinterpret_cast<uint16_t *>(p.out)[t * p.ldo + n] = bf16_bits(a);
+
+template <int NV>
+__device__ __forceinline__ void linear_bias(const float *bias, int n, int N, float (&b)[NV]) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) b[i] = bias && n < N ? __ldg(bias + min(n + i, N - 1)) : 0.f;
 }
 
 // ------------------------------------------------------ few tokens: stream --
@@ -193,18 +248,18 @@ __global__ void __launch_bounds__(512, 1) linear_stream_kernel(const __grid_cons
     for (int i = threadIdx.x; i < RG * TT * 8; i += blockDim.x) {
         const int rg = i / (TT * 8), t = (i / 8) % TT, n = n0 + rg * 8 + i % 8;
         if (t >= p.T || n >= p.N) continue;
-        const float b = p.bias ? __ldg(p.bias + n) : 0.f, bg = p.bias_g ? __ldg(p.bias_g + n) : 0.f;
-        float res[1];
-        linear_resid(p, res, t, 0, t, n);
-        float v[1] = {0.f}, gv[1] = {0.f};
+        float b[1], bg[1], v[1] = {0.f}, gv[1] = {0.f};
+        linear_bias(p.bias, n, p.N, b);
+        linear_bias(p.bias_g, n, p.N, bg);
+        Residual<1> res;
+        linear_resid(p, t, n, res, p.out_fp32);
         const float *src = red + (GATED ? 2 * rg : rg) * TT * 8 + i % (TT * 8);
 #pragma unroll 4
         for (int w = 0; w < nw; ++w) {
             v[0] += src[w * NM * TT * 8];
             if (GATED) gv[0] += src[(w * NM + 1) * TT * 8];
         }
-        linear_values(p, v, gv, b, bg, res);
-        linear_store(p, t, n, v[0]);
+        linear_finish(p, t, n, v, gv, b, bg, res, GATED, p.resid != nullptr, p.out_fp32);
     }
 }
 
@@ -305,6 +360,18 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
 
     const int half = warp >> 2, hcols = ((bn / 16 + 1) / 2) * 16;  // columns of the first of a quadrant's warps
     const int c0 = half * hcols, ncol = half ? bn - hcols : hcols;
+    // What a thread finishes: 8 rows (output columns n..n+7) of the tokens
+    // j0, j0 + step, ... of this CTA, NU at a time.  The first residuals are
+    // loaded before the sums are waited for.
+    constexpr int NU = 4;
+    const int rowg = nrow / 8, n = n0 + (threadIdx.x % rowg) * 8, j0 = threadIdx.x / rowg, step = 256 / rowg;
+    const int jmax = n < p.N && warp < 8 ? min(cpo, min(bn, p.T - t0) - rank * cpo) : 0;
+    Residual<8> res[NU];
+    auto fetch = [&](int j) {
+#pragma unroll
+        for (int i = 0; i < NU; ++i)
+            if (j0 + (j + i) * step < jmax) linear_resid(p, (long long)t0 + rank * cpo + j0 + (j + i) * step, n, res[i], p.out_fp32);
+    };
     // red[source][column][row]: the columns this CTA finishes; sum[column][row]:
     // this CTA's sums of the chains before the last (one CTA: the same buffer)
     float *red = reinterpret_cast<float *>(smem + a.red);
@@ -373,6 +440,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
             mbar_drain(mdone, 0u, a.wait_ns);
         }
     } else {
+        fetch(0);
         for (int c = 0; c < nch; ++c) {
             const int buf = c & 1;
             if (!wait(&afull[buf], (uint32_t)((c >> 1) & 1))) break;
@@ -422,31 +490,33 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
     } else {
         __syncthreads();
     }
-    const int nl = threadIdx.x & (nrow - 1), n = n0 + nl, step = 256 / nrow;
-    if (warp < 8 && n < p.N) {
-        constexpr int NV = 8;  // columns whose residuals are fetched together
-        const int jmax = min(cpo, min(bn, p.T - t0) - rank * cpo);
-        const float b = p.bias ? __ldg(p.bias + n) : 0.f;
-        const float bg = p.bias_g ? __ldg(p.bias_g + n) : 0.f;
-        for (int j0 = threadIdx.x / nrow; j0 < jmax; j0 += NV * step) {
-            const long long t = (long long)t0 + rank * cpo + j0;
-            float v[NV], g[NV], res[NV];
-            linear_resid(p, res, t, step, (long long)t0 + rank * cpo + jmax - 1, n);
+    if (jmax > 0) {
+        float b[8], bg[8];
+        linear_bias(p.bias, n, p.N, b);
+        linear_bias(p.bias_g, n, p.N, bg);
+        for (int j = 0; j0 + j * step < jmax; j += NU) {
+            if (j > 0) fetch(j);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) v[i] = g[i] = 0.f;
-            const float *r = red + nl;
-            for (int s = 0; s < S; ++s, r += cpo * 128) {
+            for (int i = 0; i < NU; ++i) {
+                const int jj = j0 + (j + i) * step;
+                if (jj < jmax) {
+                    float v[8] = {}, g[8] = {};
+                    const float *r = red + jj * 128 + (n - n0);
+                    for (int s = 0; s < S; ++s, r += cpo * 128) {
 #pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const int j = min(j0 + i * step, jmax - 1);
-                    v[i] += r[j * 128];
-                    if (gated) g[i] += r[j * 128 + 64];
+                        for (int e = 0; e < 8; e += 4) {
+                            const float4 x = *reinterpret_cast<const float4 *>(r + e);
+                            v[e] += x.x, v[e + 1] += x.y, v[e + 2] += x.z, v[e + 3] += x.w;
+                            if (gated) {
+                                const float4 y = *reinterpret_cast<const float4 *>(r + 64 + e);
+                                g[e] += y.x, g[e + 1] += y.y, g[e + 2] += y.z, g[e + 3] += y.w;
+                            }
+                        }
+                    }
+                    linear_finish(p, (long long)t0 + rank * cpo + jj, n, v, g, b, bg, res[i], gated, p.resid != nullptr,
+                                  p.out_fp32);
                 }
             }
-            linear_values(p, v, g, b, bg, res);
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (j0 + i * step < jmax) linear_store(p, t + i * step, n, v[i]);
         }
     }
     umma::fence_before();
@@ -462,9 +532,13 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
 // and half of the tokens, so every operand byte a pair brings in feeds twice
 // the MMA work of a single CTA's tile.  Two tensor-memory buffers: the
 // epilogue of a tile runs under the next tile's MMAs.
-constexpr int kLpExch = 4 * 32 * 32 * 4;  // gated: 32 x 32 fp32 for each of the four pairs of epilogue warps
+constexpr int kLpRow = 36;                  // floats from token to token of the epilogue's buffers (4 off: no bank conflicts)
+constexpr int kLpEpi = 16;                  // epilogue warps: four per lane quadrant
+constexpr int kLpThreads = 32 * (kLpEpi + 2);
+constexpr int kLpExch = kLpEpi * 16 * kLpRow * 4;
 
-__global__ void __launch_bounds__(kLtThreads, 1) linear_pair_kernel(const __grid_constant__ LinearTcParams a) {
+template <bool GATED, bool RESID>
+__global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid_constant__ LinearTcParams a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const LinearParams &p = a.p;
@@ -487,13 +561,13 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_pair_kernel(const __grid
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&afull[b], 1);
-            mbar_init(&aempty[b], 16);  // CTA 0's: the epilogue warps of both
+            mbar_init(&aempty[b], 2 * kLpEpi);  // CTA 0's: the epilogue warps of both
         }
         mbar_init(mdone, 1);
         fence_mbar_init();
         *s_abort = 0;
     }
-    if (warp == 8 && lane == 0) {
+    if (warp == kLpEpi && lane == 0) {
         prefetch_tmap(a.tw);
         prefetch_tmap(a.tx);
     }
@@ -504,8 +578,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_pair_kernel(const __grid
     umma::cluster_wait();  // both CTAs' barriers are set up
     umma::fence_after();
     const uint32_t tbase = *tslot;
-    const bool gated = p.wg != nullptr;
-    const int nrow = gated ? 64 : 128;  // output columns of one CTA's rows
+    const int nrow = GATED ? 64 : 128;  // output columns of one CTA's rows
     const int nk = ceil_div(p.K, kLtKStep);
     const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
     const int items = a.nrb * a.ntt;
@@ -521,7 +594,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_pair_kernel(const __grid
     pdl_wait();
     pdl_trigger();
 
-    if (warp == 8) {
+    if (warp == kLpEpi) {
         int i = 0, s = 0;
         uint32_t ph = 1u;
         bool ok = true;
@@ -539,7 +612,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_pair_kernel(const __grid
                     const uint32_t bar = umma::mapa(smem_u32(&full[s]), 0u);
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)(2 * SB));
                     umma::tma_load_2d_pair(st, a.tw, kt * kLtKStep, n0, bar);
-                    if (gated) umma::tma_load_2d_pair(st + kLtA / 2, a.twg, kt * kLtKStep, n0, bar);
+                    if (GATED) umma::tma_load_2d_pair(st + kLtA / 2, a.twg, kt * kLtKStep, n0, bar);
                     umma::tma_load_2d_pair(st + kLtA, a.tx, kt * kLtKStep, tx, bar);
                 }
                 __syncwarp();
@@ -555,7 +628,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_pair_kernel(const __grid
                 mbar_drain(&full[t], (uint32_t)((last / nst) & 1), a.wait_ns);
             }
         }
-    } else if (warp == 9) {
+    } else if (warp == kLpEpi + 1) {
         if (rank == 0) {
             const uint64_t adesc = umma::smem_desc(smem_u32(stages), 16u, 1024u, umma::kLayoutSw128);
             const uint32_t idesc = umma::idesc_bf16_pair(bn);
@@ -594,73 +667,74 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_pair_kernel(const __grid
         }
         wait(mdone, 0u);  // in both CTAs: the last arrival from the pair's MMAs
     } else {
-        // Epilogue: warp w takes lane quadrant w % 4 and every second group of
-        // 16 tokens.  Gated: quadrants 0, 1 hold w's rows and 2, 3 w_gate's;
-        // the warps of quadrants u and u + 2 take groups of 32 and exchange
-        // halves, so that one finishes 16 of the tokens and the other the rest.
-        const int quad = warp & 3, hv = warp >> 2;
-        float *ex = reinterpret_cast<float *>(stages + nst * SB) + ((quad & 1) * 2 + hv) * (32 * 32);
-        const int nl = gated ? 32 * (quad & 1) + lane : 32 * quad + lane;
+        // Epilogue: warp w takes lane quadrant w % 4 and every fourth group of
+        // 16 tokens, through shared memory so that a thread finishes 8
+        // neighbouring columns of a token.  Gated: quadrants 0, 1 hold w's rows
+        // and 2, 3 w_gate's; the warps of quadrants u and u + 2 write their
+        // sums of a group and finish 8 of its tokens each.
+        const int quad = warp & 3, hv = warp >> 2, peer = (quad & 1) + 2 * hv;
+        float *ex = reinterpret_cast<float *>(stages + nst * SB);
+        float *mine = ex + warp * kLpRow * 16;  // [16 tokens][32 columns]
+        const float *vs = ex + (GATED ? warp & ~2 : warp) * kLpRow * 16, *gs = ex + (warp | 2) * kLpRow * 16;
+        constexpr int np = GATED ? 1 : 2;                            // passes of 8 tokens
+        const int tl = (GATED ? (quad >> 1) * 8 : 0) + lane / 4; // first token of this thread in a group
+        const int nl = 32 * (GATED ? quad & 1 : quad) + (lane & 3) * 8;
         int q = 0;
         for (int it = pair; it < items; it += pairs, ++q) {
             int n0, t0;
             tile_at(it, n0, t0);
             const int n = n0 + nl, buf = q & 1;
-            const bool nin = n < p.N;
-            const float b = p.bias && nin ? __ldg(p.bias + n) : 0.f;
-            const float bg = p.bias_g && nin ? __ldg(p.bias_g + n) : 0.f;
-            const int left = nin ? p.T - t0 : 0;  // tokens of this tile to store
-            const uint16_t *rp = reinterpret_cast<const uint16_t *>(p.resid) + (long long)t0 * p.ldr + n;
-            uint16_t *op = reinterpret_cast<uint16_t *>(p.out) + (long long)t0 * p.ldo + n;
-            // The residuals of the 16 tokens from f on, loaded one group ahead
-            // of their use (the first while the tile's MMAs run).
-            uint16_t rn[16] = {};
+            const int left = n < p.N ? p.T - t0 : 0;  // tokens of this tile to store
+            float b[8], bg[8];
+            linear_bias(p.bias, n, p.N, b);
+            linear_bias(p.bias_g, n, p.N, bg);
+            // Residuals, one group ahead of their use (the first while the
+            // tile's MMAs run).
+            Residual<8> res[np];
             auto fetch = [&](int f) {
-                if (p.resid && f < bn && left > 0) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) rn[j] = rp[(long long)min(f + j, left - 1) * p.ldr];
-                }
+                for (int h = 0; h < np; ++h)
+                    if (RESID && f < bn && f + tl + 8 * h < left) linear_resid(p, t0 + f + tl + 8 * h, n, res[h], false);
             };
-            const bool low = quad < 2;  // gated: holds w's sums
-            const int gstep = gated ? 64 : 32, f0 = gated ? hv * 32 + (low ? 0 : 16) : hv * 16;
-            fetch(f0);
+            fetch(hv * 16);
             bool got = wait(&afull[buf], (uint32_t)((q >> 1) & 1));
             // the two warps that exchange go on together or not at all
-            if (gated) got = umma::bar_red_and(1 + (quad & 1) * 2 + hv, 64, got);
+            if (GATED) got = umma::bar_red_and(1 + peer, 64, got);
             if (!got) break;
             umma::fence_after();
             const uint32_t src = tbase + umma::lane_base(warp) + (uint32_t)(buf * 256);
-            for (int f = f0; f < bn; f += gstep) {  // the 16 tokens this warp finishes
-                float v[16], g[16], r[16];
+            for (int f = hv * 16; f < bn; f += 4 * kLpEpi) {
                 uint32_t raw[16];
                 umma::ld16(src + f, raw);
-                if (gated) {
-                    uint32_t give[16];
-                    umma::ld16(src + (low ? f + 16 : f - 16), give);
-                    umma::wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) ex[((low ? 16 : 0) + j) * 32 + lane] = __uint_as_float(give[j]);
-                    umma::bar_sync(1 + (quad & 1) * 2 + hv, 64);
-                }
                 umma::wait_ld();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float mine = __uint_as_float(raw[j]);
-                    v[j] = mine;
-                    if (gated) {
-                        const float other = ex[((low ? 0 : 16) + j) * 32 + lane];
-                        v[j] = low ? mine : other;
-                        g[j] = low ? other : mine;
-                    }
-                    r[j] = bf16_lo(rn[j]);
-                }
-                fetch(f + gstep);
-                linear_values(p, v, g, b, bg, r);
-                uint16_t *o = op + (long long)f * p.ldo;
+                for (int j = 0; j < 16; ++j) mine[j * kLpRow + lane] = __uint_as_float(raw[j]);
+                if (GATED)
+                    umma::bar_sync(1 + peer, 64);
+                else
+                    __syncwarp();
+                float v[np][8], g[np][8];
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    if (f + j < left) o[j * p.ldo] = bf16_bits(v[j]);
-                if (gated) umma::bar_sync(1 + (quad & 1) * 2 + hv, 64);
+                for (int h = 0; h < np; ++h)
+#pragma unroll
+                    for (int e = 0; e < 8; e += 4) {
+                        const int o = (tl + 8 * h) * kLpRow + (lane & 3) * 8 + e;
+                        const float4 x = *reinterpret_cast<const float4 *>(vs + o);
+                        v[h][e] = x.x, v[h][e + 1] = x.y, v[h][e + 2] = x.z, v[h][e + 3] = x.w;
+                        if (GATED) {
+                            const float4 y = *reinterpret_cast<const float4 *>(gs + o);
+                            g[h][e] = y.x, g[h][e + 1] = y.y, g[h][e + 2] = y.z, g[h][e + 3] = y.w;
+                        }
+                    }
+#pragma unroll
+                for (int h = 0; h < np; ++h)
+                    if (f + tl + 8 * h < left)
+                        linear_finish(p, (long long)t0 + f + tl + 8 * h, n, v[h], g[h], b, bg, res[h], GATED, RESID, false);
+                fetch(f + 4 * kLpEpi);
+                if (GATED)
+                    umma::bar_sync(1 + peer, 64);
+                else
+                    __syncwarp();
             }
             umma::fence_before();
             __syncwarp();
