@@ -135,18 +135,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) pf_expert_kernel(const __grid_c
     const uint32_t sf0 = (uint32_t)(NBUF * NMAT * kPfN);
     auto item_of = [&](int q) { return cta + q * G; };
     auto nk_of = [&](int it) { return it < IR ? nkt : nkts; };
-    auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (*s_abort) return false;
-        if (mbar_wait_bounded(bar, parity, hdr, p.wait_ns)) return true;
-        *s_abort = 1;
-        return false;
-    };
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait_warp(bar, parity, hdr, p.wait_ns, s_abort); };
     // the q-th item's description is in slot q % kPfSlots once mfull says so
     auto slot_wait = [&](int q) -> PfSlot * {
-        int go = 0;
-        if (lane == 0) go = wait(&mfull[q % kPfSlots], (uint32_t)((q / kPfSlots) & 1));
-        go = __shfl_sync(0xffffffffu, go, 0);
-        return go ? &slots[q % kPfSlots] : nullptr;
+        return wait(&mfull[q % kPfSlots], (uint32_t)((q / kPfSlots) & 1)) ? &slots[q % kPfSlots] : nullptr;
     };
     auto slot_done = [&](int q) {
         __syncwarp();
@@ -186,9 +178,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) pf_expert_kernel(const __grid_c
             r1 = r2;
             if (q + 2 < nmine) r2 = __ldcg(items + item_of(q + 2));
             if (q + 1 < nmine) pairs_of(r1, pid1, w1);
-            int go = 1;
-            if (lane == 0 && q >= kPfSlots) go = wait(&mempty[q % kPfSlots], (uint32_t)(((q / kPfSlots) + 1) & 1));
-            if (!__shfl_sync(0xffffffffu, go, 0)) break;
+            if (q >= kPfSlots && !wait(&mempty[q % kPfSlots], (uint32_t)(((q / kPfSlots) + 1) & 1))) break;
             PfSlot &sl = slots[q % kPfSlots];
             sl.pair[lane] = pid;
             sl.orow[lane] = rec.y >= 0 ? pid + pid / p.k : pid * (p.k + 1) + p.k;
@@ -233,13 +223,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) pf_expert_kernel(const __grid_c
             }
             const int nk = nk_of(it);
             for (int kt = 0; kt < nk; ++kt, ++it_stage) {
-                int go = 1;
-                if (lane == 0 && it_stage >= nst) go = wait(&empty[s], ph ^ 1u);
-                if (!__shfl_sync(0xffffffffu, go, 0)) break;
+                if (it_stage >= nst && !wait(&empty[s], ph ^ 1u)) break;
                 uint8_t *st = smem + s * SB;
                 uint8_t *bdst = st + NMAT * kAtile;
                 uint8_t *sfb = st + pf_sfb_off(GU);
-                if (lane == 0) {
+                if (umma::elect()) {
                     uint32_t tx;
                     if (shared) {
                         tx = (uint32_t)(NMAT * kAtile + NS * 128);
@@ -300,9 +288,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) pf_expert_kernel(const __grid_c
             const int nk = nk_of(it);
             bool go = true;
             for (int kt = 0; kt < nk; ++kt) {
-                int w0 = 0;
-                if (lane == 0) w0 = wait(&full[s], ph);
-                if (!__shfl_sync(0xffffffffu, w0, 0)) {
+                if (!wait(&full[s], ph)) {
                     go = false;
                     break;
                 }
@@ -361,34 +347,35 @@ __global__ void __launch_bounds__(kPfThreads, 1) pf_expert_kernel(const __grid_c
         if (p.strict && __any_sync(0xffffffffu, nanb != 0u) && lane == 0) set_status(hdr, kStDeviceCheck);
     } else if (warp == 9) {
         // ------------------------------------------------- MMA issuer --
-        if (lane == 0) {
-            const uint32_t bbase = smem_u32(smem) + NMAT * kAtile;
-            const uint64_t adesc0 = umma::smem_desc(smem_u32(smem), 16u, 1024u, umma::kLayoutSw128);
-            const uint64_t bdesc0 = umma::smem_desc(bbase, (uint32_t)((kPfN / 8) * 128), 128u, umma::kLayoutNone);
-            const uint32_t bstep = (uint32_t)(2 * (kPfN / 8) * 128) >> 4;
-            const uint64_t bdesc0s = umma::smem_desc(bbase, (uint32_t)((NS / 8) * 128), 128u, umma::kLayoutNone);
-            const uint32_t bsteps = (uint32_t)(2 * (NS / 8) * 128) >> 4;
-            const uint32_t id4[2] = {umma::idesc_sf_id(idesc4, 0u), umma::idesc_sf_id(idesc4, 2u)};
-            int s = 0;
-            uint32_t ph = 0u;
-            for (int q = 0; q < nmine && !*s_abort; ++q) {
-                const int it = item_of(q);
-                const bool shared = it >= IR;
-                const int buf = q % NBUF;
-                if (q >= NBUF && !wait(&aempty[buf], (uint32_t)(((q / NBUF) + 1) & 1))) break;
+        const uint32_t bbase = smem_u32(smem) + NMAT * kAtile;
+        const uint64_t adesc0 = umma::smem_desc(smem_u32(smem), 16u, 1024u, umma::kLayoutSw128);
+        const uint64_t bdesc0 = umma::smem_desc(bbase, (uint32_t)((kPfN / 8) * 128), 128u, umma::kLayoutNone);
+        const uint32_t bstep = (uint32_t)(2 * (kPfN / 8) * 128) >> 4;
+        const uint64_t bdesc0s = umma::smem_desc(bbase, (uint32_t)((NS / 8) * 128), 128u, umma::kLayoutNone);
+        const uint32_t bsteps = (uint32_t)(2 * (NS / 8) * 128) >> 4;
+        const uint32_t id4[2] = {umma::idesc_sf_id(idesc4, 0u), umma::idesc_sf_id(idesc4, 2u)};
+        int s = 0;
+        uint32_t ph = 0u;
+        bool go = true;
+        for (int q = 0; q < nmine && go; ++q) {
+            const int it = item_of(q);
+            const bool shared = it >= IR;
+            const int buf = q % NBUF;
+            if (q >= NBUF && !wait(&aempty[buf], (uint32_t)(((q / NBUF) + 1) & 1))) break;
+            umma::fence_after();
+            const uint32_t dcol = tbase + (uint32_t)(buf * NMAT * kPfN);
+            const int nk = nk_of(it);
+            for (int kt = 0; kt < nk; ++kt) {
+                if (!wait(&full[s], ph) || !wait(&sfr[s], ph)) {
+                    go = false;
+                    break;
+                }
                 umma::fence_after();
-                const uint32_t dcol = tbase + (uint32_t)(buf * NMAT * kPfN);
-                uint32_t acc = 0u;
-                const int nk = nk_of(it);
-                bool go = true;
-                for (int kt = 0; kt < nk; ++kt) {
-                    if (!wait(&full[s], ph) || !wait(&sfr[s], ph)) {
-                        go = false;
-                        break;
-                    }
-                    umma::fence_after();
-                    const uint32_t soff = (uint32_t)(s * SB) >> 4;
-                    const uint64_t a0 = adesc0 + soff;
+                const uint32_t soff = (uint32_t)(s * SB) >> 4;
+                const uint64_t a0 = adesc0 + soff;
+                // one lane issues, the loop around it is warp-uniform: the
+                // operands stay in uniform registers
+                if (umma::elect()) {
                     if (shared) {
                         const uint64_t b0 = bdesc0s + soff;
                         const int nks = min(4, (Ks - kt * kTileKs) / 16);
@@ -396,9 +383,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) pf_expert_kernel(const __grid_c
                         for (int sk = 0; sk < 4; ++sk) {
                             if (sk < nks) {
                                 const uint64_t bd = b0 + sk * bsteps;
+                                const uint32_t acc = kt > 0 || sk > 0 ? 1u : 0u;
                                 umma::mma_bf16(dcol, a0 + 2 * sk, bd, idesc16, acc);
                                 if (GU) umma::mma_bf16(dcol + kPfN, a0 + (kAtile >> 4) + 2 * sk, bd, idesc16, acc);
-                                acc = 1u;
                             }
                         }
                     } else {
@@ -411,25 +398,28 @@ __global__ void __launch_bounds__(kPfThreads, 1) pf_expert_kernel(const __grid_c
                                 const uint64_t bd = b0 + sk * bstep;
                                 const uint32_t sfid = (uint32_t)(2 * (sk & 1)) << 30;
                                 const uint32_t sfb = (sfc + 8 * NMAT + (sk >> 1) * 4) | sfid;
+                                const uint32_t acc = kt > 0 || sk > 0 ? 1u : 0u;
                                 umma::mma_mxf4(dcol, a0 + 2 * sk, bd, id4[sk & 1], acc, (sfc + (sk >> 1) * 4) | sfid, sfb);
                                 if (GU)
                                     umma::mma_mxf4(dcol + kPfN, a0 + (kAtile >> 4) + 2 * sk, bd, id4[sk & 1], acc,
                                                    (sfc + 8 + (sk >> 1) * 4) | sfid, sfb);
-                                acc = 1u;
                             }
                         }
                     }
                     umma::commit(&empty[s]);
-                    if (++s == nst) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
                 }
-                umma::commit(&afull[buf]);
-                if (!go) break;
+                __syncwarp();
+                if (++s == nst) {
+                    s = 0;
+                    ph ^= 1u;
+                }
             }
-            // the CTA frees its tensor memory only after every MMA issued here
-            // has completed (on an early exit too)
+            if (umma::elect()) umma::commit(&afull[buf]);
+            __syncwarp();
+        }
+        // the CTA frees its tensor memory only after every MMA issued here
+        // has completed (on an early exit too)
+        if (umma::elect()) {
             umma::commit(mdone);
             mbar_drain(mdone, 0u, p.wait_ns);
         }
@@ -445,9 +435,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) pf_expert_kernel(const __grid_c
             const int buf = q % NBUF;
             const int n = sl->n, rb = sl->rb;
             const bool ok = sl->ok != 0;
-            int go = 0;
-            if (lane == 0) go = wait(&afull[buf], (uint32_t)((q / NBUF) & 1));
-            go = __shfl_sync(0xffffffffu, go, 0);
+            const bool go = wait(&afull[buf], (uint32_t)((q / NBUF) & 1));
             umma::fence_after();
             float acc[NMAT][kGroup];
             if (!shared) {

@@ -779,72 +779,84 @@ __global__ void __launch_bounds__(kUThreads, 1) umma_expert_kernel(const __grid_
         if (p.strict && __any_sync(0xffffffffu, nanb != 0u) && lane == 0) set_status(hdr, kStDeviceCheck);
     } else if (warp == 9) {
         // ------------------------------------------------- MMA issuer --
-        // One thread; everything per MMA is an add on precomputed descriptors
-        // (the start-address field of a descriptor is its low 14 bits, and
-        // every operand address here stays below 256 KB).
-        if (lane == 0) {
-            const uint64_t adesc0 = umma::smem_desc(smem_u32(smem), 16u, 1024u, umma::kLayoutSw128);
-            const uint64_t bdesc0 = umma::smem_desc(smem_u32(smem) + NMAT * kAtile, (uint32_t)((N / 8) * 128), 128u,
-                                                    umma::kLayoutNone);
-            const uint32_t bstep = (uint32_t)(2 * (N / 8) * 128) >> 4;  // one k-step of B (2 chunks)
-            const uint32_t id4[2] = {umma::idesc_sf_id(idesc4, 0u), umma::idesc_sf_id(idesc4, 2u)};
-            int seg = 0, s = 0;
-            uint32_t ph = 0u;
-            for (int ri = 0; ri < 2 && !*s_abort; ++ri) {
-            if (ri == 1 && (!GU || !routed_range(false))) break;
+        // The loops are warp-uniform and one elected lane issues, so operands
+        // stay in uniform registers; everything per MMA is an add on
+        // precomputed descriptors (the start-address field of a descriptor is
+        // its low 14 bits, and every operand address here stays below 256 KB).
+        const uint64_t adesc0 = umma::smem_desc(smem_u32(smem), 16u, 1024u, umma::kLayoutSw128);
+        const uint64_t bdesc0 = umma::smem_desc(smem_u32(smem) + NMAT * kAtile, (uint32_t)((N / 8) * 128), 128u,
+                                                umma::kLayoutNone);
+        const uint32_t bstep = (uint32_t)(2 * (N / 8) * 128) >> 4;  // one k-step of B (2 chunks)
+        const uint32_t id4[2] = {umma::idesc_sf_id(idesc4, 0u), umma::idesc_sf_id(idesc4, 2u)};
+        auto waitw = [&](uint64_t *bar, uint32_t parity) { return mbar_wait_warp(bar, parity, hdr, p.wait_ns, s_abort); };
+        int seg = 0, s = 0;
+        uint32_t ph = 0u;
+        bool go = true;
+        for (int ri = 0; ri < 2 && go; ++ri) {
+            if (ri == 1 && (!GU || !routed_range(true))) break;
             const Range rg = rng(ri);
-            for (int unit = rg.a; unit < rg.b && !*s_abort; ++seg) {
+            for (int unit = rg.a; unit < rg.b && go; ++seg) {
                 Unit x = decode(unit);
                 const int seg_end = min(rg.b, x.iend);
                 const int buf = seg & 1;
-                if (seg >= 2 && !wait(&aempty[buf], (uint32_t)(((seg >> 1) + 1) & 1))) break;
+                if (seg >= 2 && !waitw(&aempty[buf], (uint32_t)(((seg >> 1) + 1) & 1))) {
+                    go = false;
+                    break;
+                }
                 umma::fence_after();
                 const uint32_t dcol = tbase + (uint32_t)(buf * NMAT * 64);
-                uint32_t acc = 0u;
                 for (int un = unit; un < seg_end; x = advance(x, ++un, rg.b)) {
-                    if (!wait(&full[s], ph) || !wait(&sfr[s], ph)) break;
+                    if (!waitw(&full[s], ph) || !waitw(&sfr[s], ph)) {
+                        go = false;
+                        break;
+                    }
                     umma::fence_after();
                     const uint32_t soff = (uint32_t)(s * SB) >> 4;
                     const uint64_t a0 = adesc0 + soff, b0 = bdesc0 + soff;
                     const int nks = ksteps(x);
-                    if (x.shared) {
+                    if (umma::elect()) {
+                        if (x.shared) {
 #pragma unroll
-                        for (int sk = 0; sk < 4; ++sk) {
-                            if (sk < nks) {
-                                const uint64_t bd = b0 + sk * bstep;
-                                umma::mma_bf16(dcol, a0 + 2 * sk, bd, idesc16, acc);
-                                umma::mma_bf16(dcol + 64, a0 + (kAtile >> 4) + 2 * sk, bd, idesc16, acc);
-                                acc = 1u;
+                            for (int sk = 0; sk < 4; ++sk) {
+                                if (sk < nks) {
+                                    const uint64_t bd = b0 + sk * bstep;
+                                    const uint32_t acc = un > unit || sk > 0 ? 1u : 0u;
+                                    umma::mma_bf16(dcol, a0 + 2 * sk, bd, idesc16, acc);
+                                    umma::mma_bf16(dcol + 64, a0 + (kAtile >> 4) + 2 * sk, bd, idesc16, acc);
+                                }
+                            }
+                        } else {
+                            const uint32_t sfc = tbase + sf0 + (uint32_t)(s * SFC);
+#pragma unroll
+                            for (int sk = 0; sk < 4; ++sk) {
+                                if (sk < nks) {
+                                    const uint64_t bd = b0 + sk * bstep;
+                                    const uint32_t sfid = (uint32_t)(2 * (sk & 1)) << 30;
+                                    const uint32_t sfb = (sfc + 8 * NMAT + (sk >> 1) * 4) | sfid;
+                                    const uint32_t acc = un > unit || sk > 0 ? 1u : 0u;
+                                    umma::mma_mxf4(dcol, a0 + 2 * sk, bd, id4[sk & 1], acc, (sfc + (sk >> 1) * 4) | sfid,
+                                                   sfb);
+                                    umma::mma_mxf4(dcol + 64, a0 + (kAtile >> 4) + 2 * sk, bd, id4[sk & 1], acc,
+                                                   (sfc + 8 + (sk >> 1) * 4) | sfid, sfb);
+                                }
                             }
                         }
-                    } else {
-                        const uint32_t sfc = tbase + sf0 + (uint32_t)(s * SFC);
-#pragma unroll
-                        for (int sk = 0; sk < 4; ++sk) {
-                            if (sk < nks) {
-                                const uint64_t bd = b0 + sk * bstep;
-                                const uint32_t sfid = (uint32_t)(2 * (sk & 1)) << 30;
-                                const uint32_t sfb = (sfc + 8 * NMAT + (sk >> 1) * 4) | sfid;
-                                umma::mma_mxf4(dcol, a0 + 2 * sk, bd, id4[sk & 1], acc, (sfc + (sk >> 1) * 4) | sfid,
-                                               sfb);
-                                umma::mma_mxf4(dcol + 64, a0 + (kAtile >> 4) + 2 * sk, bd, id4[sk & 1], acc,
-                                               (sfc + 8 + (sk >> 1) * 4) | sfid, sfb);
-                                acc = 1u;
-                            }
-                        }
+                        umma::commit(&empty[s]);
                     }
-                    umma::commit(&empty[s]);
+                    __syncwarp();
                     if (++s == nst) {
                         s = 0;
                         ph ^= 1u;
                     }
                 }
-                umma::commit(&afull[buf]);
+                if (umma::elect()) umma::commit(&afull[buf]);
+                __syncwarp();
                 unit = seg_end;
             }
-            }
-            // the CTA frees its tensor memory only after every MMA issued here
-            // has completed (on an early exit too)
+        }
+        // the CTA frees its tensor memory only after every MMA issued here
+        // has completed (on an early exit too)
+        if (umma::elect()) {
             umma::commit(mdone);
             mbar_drain(mdone, 0u, p.wait_ns);
         }
