@@ -14,110 +14,392 @@ struct GateParams {
     int T, E, k;
     const float *bias;   // fp32 [E] or null
     int sigmoid, groups, kept, group_top, renorm, bf16;
+    int vec;             // four logits of a row (and the bias) can be loaded at once
     float scale;
     int32_t *idx;        // [T][k]
     float *weight;       // [T][k]
 };
 
-// One warp per token, the values it ranks by in shared memory as 64-bit
-// numbers; every pick is a warp-wide maximum over them.
-__global__ void __launch_bounds__(32) gate_kernel(const __grid_constant__ GateParams p) {
-    __shared__ double s_order[kGateMaxE];  // c_e, or the logit where there is no bias; -inf: out
-    __shared__ float s_l[kGateMaxE];
-    __shared__ double s_group[32];
-    __shared__ float s_w[kGateMaxK];
-    const int lane = threadIdx.x;
+__device__ __forceinline__ float gate_logit(const GateParams &p, long long t, int e) {
+    return p.bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p.logits)[t * p.ld + e])
+                  : reinterpret_cast<const float *>(p.logits)[t * p.ld + e];
+}
+
+__device__ __forceinline__ double warp_sum(double v) {
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// One token in 64 bits throughout, by one warp: what the definition says, one
+// pick after the other.  The tokens that gate_kernel cannot settle in 32 bits
+// come here.
+struct GateExact {
+    double order[kGateMaxE];  // c_e, or the logit where there is no bias; -inf: out
+    float l[kGateMaxE];
+    double group[32];
+};
+__device__ __noinline__ void gate_exact(const GateParams &p, long long t, GateExact &s) {
+    const int lane = threadIdx.x & 31;
     const double ninf = -INFINITY;
-    for (long long t = blockIdx.x; t < p.T; t += gridDim.x) {
-        float mx = -INFINITY;
-        bool any_nan = false;
-        for (int e = lane; e < p.E; e += 32) {
-            const float l = p.bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p.logits)[t * p.ld + e])
-                                   : reinterpret_cast<const float *>(p.logits)[t * p.ld + e];
-            s_l[e] = l;
-            any_nan |= l != l;
-            mx = fmaxf(mx, l);
+    float mx = -INFINITY;
+    bool any_nan = false;
+    for (int e = lane; e < p.E; e += 32) {
+        const float l = gate_logit(p, t, e);
+        s.l[e] = l;
+        any_nan |= l != l;
+        mx = fmaxf(mx, l);
+    }
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const bool bad = __any_sync(0xffffffffu, any_nan) || mx == INFINITY;  // the softmax is NaN
+    double sum = 0.0;
+    if (!p.sigmoid) {
+        for (int e = lane; e < p.E; e += 32)
+            if (s.l[e] > -INFINITY) sum += exp((double)s.l[e] - (double)mx);
+        sum = warp_sum(sum);
+    }
+    auto score = [&](int e) -> double {
+        const double l = s.l[e];
+        if (p.sigmoid) return 1.0 / (1.0 + exp(-l));
+        return bad ? (double)NAN : exp(l - (double)mx) / sum;
+    };
+    for (int e = lane; e < p.E; e += 32) {
+        double c = s.l[e];
+        if (p.bias && c > ninf) c = score(e) + (double)p.bias[e];
+        s.order[e] = c > ninf && s.l[e] > -INFINITY ? c : ninf;
+    }
+    __syncwarp();
+    if (p.groups > 1) {
+        const int gs = p.E / p.groups;
+        if (lane < p.groups) {
+            double a = ninf, b = ninf;
+            for (int e = lane * gs; e < (lane + 1) * gs; ++e) {
+                double c = s.order[e];
+                if (c > ninf && !p.bias && p.group_top > 1) {
+                    c = score(e);
+                    if (!(c > ninf)) c = ninf;
+                }
+                if (c > a) {
+                    b = a;
+                    a = c;
+                } else if (c > b) {
+                    b = c;
+                }
+            }
+            s.group[lane] = p.group_top > 1 ? (b > ninf ? a + b : ninf) : a;
         }
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const bool bad = __any_sync(0xffffffffu, any_nan) || mx == INFINITY;  // the softmax is NaN
-        double sum = 0.0;
+        __syncwarp();
+        if (lane < p.groups) {
+            int r = 0;
+            for (int g = 0; g < p.groups; ++g)
+                r += s.group[g] > s.group[lane] || (s.group[g] == s.group[lane] && g < lane) ? 1 : 0;
+            if (r >= p.kept)
+                for (int e = lane * gs; e < (lane + 1) * gs; ++e) s.order[e] = ninf;
+        }
+        __syncwarp();
+    }
+    int mine = -1;  // lane j: pick j
+    for (int j = 0; j < p.k; ++j) {
+        double best = ninf;
+        int at = 0x7FFFFFFF;
+        for (int e = lane; e < p.E; e += 32)
+            if (s.order[e] > best) {
+                best = s.order[e];
+                at = e;
+            }
+        for (int o = 16; o > 0; o >>= 1) {
+            const double v = __shfl_xor_sync(0xffffffffu, best, o);
+            const int a = __shfl_xor_sync(0xffffffffu, at, o);
+            if (v > best || (v == best && a < at)) {
+                best = v;
+                at = a;
+            }
+        }
+        if (!(best > ninf)) break;
+        if (lane == j) mine = at;
+        if (lane == (at & 31)) s.order[at] = ninf;
+        __syncwarp();
+    }
+    const double w = mine >= 0 ? score(mine) : 0.0;
+    const double z = warp_sum(w);
+    if (lane < p.k) {
+        p.idx[t * p.k + lane] = mine;
+        p.weight[t * p.k + lane] = (float)((p.renorm ? (z == 0.0 ? 0.0 : w / z) : w) * (double)p.scale);
+    }
+}
+
+// One warp per token, its logits in registers (lane l holds ids 128 i + 4 l ..
+// + 3).  The selection is a filter with an error bound:
+//   - without a bias the ranking is the logits' own and exact; with one the
+//     values c_e are formed in 32 bits, each within eps of the true one;
+//   - the k-th largest of the 32 lanes' maxima is a value that at least k
+//     values reach, so only those no more than 2 eps below it can be among the
+//     k largest (about 22 of 896 for k = 16): they go to shared memory;
+//   - each candidate's place is the number of larger ones (ties to the lower
+//     id); where two neighbours of the list are within 2 eps, the candidates'
+//     values are formed again in 64 bits and placed by those.
+// What cannot be settled so (groups whose values are within the error, more
+// than kGateCap candidates, infinite biases, scores below 2^-100) goes through
+// gate_exact, so the result is that of the 64-bit definition in every case.
+// Weights are 32-bit: the scores of the picks from expf, the softmax's argument
+// l - max with its rounding error carried along.
+constexpr int kGateWarps = 4;
+constexpr int kGateCap = 256;
+struct alignas(16) GateWarp {
+    uint64_t key[kGateCap];   // value (order-preserving bits) above the inverted id
+    double exact[kGateCap];
+    float top[32];
+    float sorted[kGateMaxK + 1];
+    int32_t id[kGateMaxK + 1];
+};
+static_assert(sizeof(GateExact) % 16 == 0 && sizeof(GateWarp) % 16 == 0, "16-byte parts of shared memory");
+
+__host__ __device__ inline int gate_smem(int E, int groups) {
+    return (int)sizeof(GateExact) + kGateWarps * ((int)sizeof(GateWarp) + (groups > 1 ? E * 4 : 0));
+}
+
+__device__ __forceinline__ uint32_t order_bits(float v) {
+    const uint32_t b = __float_as_uint(v);
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float from_order_bits(uint32_t b) {
+    return __uint_as_float(b & 0x80000000u ? b ^ 0x80000000u : ~b);
+}
+
+template <int NI, bool BIAS>
+__global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_constant__ GateParams p) {
+    extern __shared__ __align__(16) uint8_t gate_raw[];
+    constexpr int N = 4 * NI;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    GateExact &slow = *reinterpret_cast<GateExact *>(gate_raw);
+    GateWarp &s = reinterpret_cast<GateWarp *>(gate_raw + sizeof(GateExact))[warp];
+    float *gbuf = reinterpret_cast<float *>(gate_raw + sizeof(GateExact) + kGateWarps * sizeof(GateWarp)) + warp * p.E;
+    const long long t = (long long)blockIdx.x * kGateWarps + warp;
+    const float ninf = -INFINITY;
+    const uint32_t all = 0xffffffffu;
+    pdl_wait();
+    pdl_trigger();
+    bool unsettled = false;
+    if (t < p.T) {
+        float l[N], o[N];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int e = 128 * i + 4 * lane;
+            if (p.vec && e + 4 <= p.E) {
+                if (p.bf16) {
+                    const uint2 v = *reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(p.logits) + t * p.ld + e);
+                    l[4 * i] = bf16_lo(v.x), l[4 * i + 1] = bf16_hi(v.x), l[4 * i + 2] = bf16_lo(v.y), l[4 * i + 3] = bf16_hi(v.y);
+                } else {
+                    const float4 v = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p.logits) + t * p.ld + e);
+                    l[4 * i] = v.x, l[4 * i + 1] = v.y, l[4 * i + 2] = v.z, l[4 * i + 3] = v.w;
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) l[4 * i + c] = e + c < p.E ? gate_logit(p, t, e + c) : ninf;
+            }
+            if (BIAS) {
+                if (p.vec && e + 4 <= p.E) {
+                    const float4 v = *reinterpret_cast<const float4 *>(p.bias + e);
+                    o[4 * i] = v.x, o[4 * i + 1] = v.y, o[4 * i + 2] = v.z, o[4 * i + 3] = v.w;
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) o[4 * i + c] = e + c < p.E ? p.bias[e + c] : 0.f;
+                }
+            }
+        }
+        float mx = ninf;
+#pragma unroll
+        for (int i = 0; i < N; ++i) mx = fmaxf(mx, l[i]);  // passes over NaN
+        for (int q = 16; q > 0; q >>= 1) mx = fmaxf(mx, __shfl_xor_sync(all, mx, q));
+        float sum = 0.f, inv = 0.f;
         if (!p.sigmoid) {
-            for (int e = lane; e < p.E; e += 32)
-                if (s_l[e] > -INFINITY) sum += exp((double)s_l[e] - (double)mx);
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            // NaN and +inf logits make it NaN, as the formula does; __expf's
+            // error (2 units and |x| half units) is small where the term is
+            if (mx > ninf) {
+                float part[4] = {};
+#pragma unroll
+                for (int i = 0; i < N; ++i) part[i % 4] += __expf(l[i] - mx);
+                sum = (part[0] + part[1]) + (part[2] + part[3]);
+                for (int q = 16; q > 0; q >>= 1) sum += __shfl_xor_sync(all, sum, q);
+                inv = 1.0f / sum;  // the largest score
+            }
         }
-        auto score = [&](int e) -> double {
-            const double l = s_l[e];
-            if (p.sigmoid) return 1.0 / (1.0 + exp(-l));
-            return bad ? (double)NAN : exp(l - (double)mx) / sum;
-        };
-        for (int e = lane; e < p.E; e += 32) {
-            double c = s_l[e];
-            if (p.bias && c > ninf) c = score(e) + (double)p.bias[e];
-            s_order[e] = c > ninf && s_l[e] > -INFINITY ? c : ninf;
+        // A score in 32 bits: within 2^-20 (sigmoid) or 2^-18 of the largest (softmax).
+        auto rough = [&](float v) { return p.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-v)) : __expf(v - mx) * inv; };
+        const float rough_eps = p.sigmoid ? 0x1p-20f : inv * 0x1p-18f;
+        float eps = 0.f, amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (BIAS) {
+                const float c = rough(l[i]) + o[i];
+                o[i] = l[i] > ninf && c > ninf ? c + 0.f : ninf;
+                if (o[i] > ninf) amax = fmaxf(amax, fabsf(o[i]));
+            } else {
+                o[i] = l[i] > ninf ? l[i] + 0.f : ninf;  // -0 ranks as 0
+            }
         }
-        __syncwarp();
+        if (BIAS) {
+            for (int q = 16; q > 0; q >>= 1) amax = fmaxf(amax, __shfl_xor_sync(all, amax, q));
+            eps = rough_eps + 0x1p-23f * amax;
+            if (!(eps < 0x1p100f)) {
+                unsettled = amax > 0.f;  // infinite biases; without one: NaN scores, no expert left
+                eps = 0.f;
+            }
+        }
         if (p.groups > 1) {
+            // lanes-per-group lanes scan a group for its one or two largest values
             const int gs = p.E / p.groups;
-            if (lane < p.groups) {
-                double a = ninf, b = ninf;
-                for (int e = lane * gs; e < (lane + 1) * gs; ++e) {
-                    double c = s_order[e];
-                    if (c > ninf && !p.bias && p.group_top > 1) {
-                        c = score(e);
-                        if (!(c > ninf)) c = ninf;
-                    }
-                    if (c > a) {
-                        b = a;
-                        a = c;
-                    } else if (c > b) {
-                        b = c;
-                    }
+            const bool scores = !BIAS && p.group_top > 1;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int e = 128 * (i / 4) + 4 * lane + i % 4;
+                float v = o[i];
+                if (scores && v > ninf) {
+                    v = rough(l[i]);
+                    if (!(v > ninf)) v = ninf;
                 }
-                s_group[lane] = p.group_top > 1 ? (b > ninf ? a + b : ninf) : a;
+                if (e < p.E) gbuf[e] = v;
             }
             __syncwarp();
-            bool keep = false;
-            if (lane < p.groups) {
-                int r = 0;
-                for (int g = 0; g < p.groups; ++g)
-                    r += s_group[g] > s_group[lane] || (s_group[g] == s_group[lane] && g < lane) ? 1 : 0;
-                keep = r < p.kept;
-                if (!keep)
-                    for (int e = lane * gs; e < (lane + 1) * gs; ++e) s_order[e] = ninf;
-            }
-            __syncwarp();
-        }
-        int mine = -1;  // lane j: pick j
-        for (int j = 0; j < p.k; ++j) {
-            double best = ninf;
-            int at = 0x7FFFFFFF;
-            for (int e = lane; e < p.E; e += 32)
-                if (s_order[e] > best) {
-                    best = s_order[e];
-                    at = e;
+            int lp = 32;
+            while (lp * p.groups > 32) lp >>= 1;
+            const int g = lane / lp;
+            float a = ninf, b = ninf;
+            if (g < p.groups)
+                for (int e = lane % lp; e < gs; e += lp) {
+                    const float v = gbuf[g * gs + e];
+                    b = fmaxf(b, fminf(a, v));
+                    a = fmaxf(a, v);
                 }
-            for (int o = 16; o > 0; o >>= 1) {
-                const double v = __shfl_xor_sync(0xffffffffu, best, o);
-                const int a = __shfl_xor_sync(0xffffffffu, at, o);
-                if (v > best || (v == best && a < at)) {
-                    best = v;
-                    at = a;
-                }
+            for (int q = 1; q < lp; q <<= 1) {
+                const float a2 = __shfl_xor_sync(all, a, q), b2 = __shfl_xor_sync(all, b, q);
+                b = fmaxf(fmaxf(b, b2), fminf(a, a2));
+                a = fmaxf(a, a2);
             }
-            if (!(best > ninf)) break;
-            if (lane == j) mine = at;
-            if (lane == (at & 31)) s_order[at] = ninf;
-            __syncwarp();
+            float v = p.group_top > 1 ? (b > ninf ? a + b : ninf) : a;
+            v = __shfl_sync(all, v, (lane * lp) & 31);
+            int r = 0;
+            for (int h = 0; h < p.groups; ++h) {
+                const float x = __shfl_sync(all, v, h);
+                r += x > v || (x == v && h < lane) ? 1 : 0;
+            }
+            const bool is = lane < p.groups;
+            const uint32_t keep = __ballot_sync(all, is && r < p.kept);
+            if (BIAS || scores) {
+                // the last group kept and the first one dropped must differ by more than their errors
+                const float vk = __shfl_sync(all, v, __ffs(__ballot_sync(all, is && r == p.kept - 1)) - 1);
+                const float vd = __shfl_sync(all, v, __ffs(__ballot_sync(all, is && r == p.kept)) - 1);
+                const float geps = p.group_top * (BIAS ? eps : rough_eps) + 0x1p-23f * fmaxf(fabsf(vk), fabsf(vd));
+                if (vk > ninf && vd > ninf && !(vk - vd > 2.f * geps)) unsettled = true;
+            }
+            const uint32_t m = (0x100000u + gs - 1) / gs;  // e / gs = e m >> 20 for e < 1024
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const uint32_t e = 128 * (i / 4) + 4 * lane + i % 4;
+                if (!((keep >> ((e * m) >> 20 & 31)) & 1u)) o[i] = ninf;
+            }
         }
-        const double w = mine >= 0 ? score(mine) : 0.0;
-        double z = w;
-        for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-        if (lane < p.k) {
-            p.idx[t * p.k + lane] = mine;
-            p.weight[t * p.k + lane] = (float)((p.renorm ? (z == 0.0 ? 0.0 : w / z) : w) * (double)p.scale);
-        }
+        // the k-th largest lane maximum
+        float lm = ninf;
+#pragma unroll
+        for (int i = 0; i < N; ++i) lm = fmaxf(lm, o[i]);
+        s.top[lane] = lm;
         __syncwarp();
+        int r = 0;
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(&s.top[j]);
+            r += (v.x > lm || (v.x == lm && j < lane)) + (v.y > lm || (v.y == lm && j + 1 < lane)) +
+                 (v.z > lm || (v.z == lm && j + 2 < lane)) + (v.w > lm || (v.w == lm && j + 3 < lane));
+        }
+        const float th = __shfl_sync(all, lm, __ffs(__ballot_sync(all, r == p.k - 1)) - 1) - 2.f * eps;
+        // candidates
+        int cnt = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) cnt += o[i] > ninf && o[i] >= th ? 1 : 0;
+        int pos = cnt;
+#pragma unroll
+        for (int q = 1; q < 32; q <<= 1) {
+            const int v = __shfl_up_sync(all, pos, q);
+            if (lane >= q) pos += v;
+        }
+        const int C = __shfl_sync(all, pos, 31);
+        pos -= cnt;
+        if (C > kGateCap) unsettled = true;
+        if (!unsettled) {  // alike in all lanes
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (o[i] > ninf && o[i] >= th)
+                    s.key[pos++] = (uint64_t)order_bits(o[i]) << 32 | (uint32_t)~(128 * (i / 4) + 4 * lane + i % 4);
+            __syncwarp();
+            for (int c = lane; c < C; c += 32) {
+                const uint64_t key = s.key[c];
+                int place = 0;
+                for (int j = 0; j < C; ++j) place += s.key[j] > key ? 1 : 0;
+                if (place <= p.k) {
+                    s.sorted[place] = from_order_bits((uint32_t)(key >> 32));
+                    s.id[place] = (int32_t)~(uint32_t)key;
+                }
+            }
+            __syncwarp();
+            const int got = min(C, p.k);
+            if (BIAS) {
+                const bool close = lane < got && lane + 1 < C && !(s.sorted[lane] - s.sorted[lane + 1] > 2.f * eps);
+                if (__any_sync(all, close)) {
+                    double sum64 = 0.0;
+                    if (!p.sigmoid) {
+                        // in gate_exact's order: ids lane, lane + 32, ...
+                        for (int e = lane; e < p.E; e += 32) {
+                            const float v = gate_logit(p, t, e);
+                            if (v > ninf) sum64 += exp((double)v - (double)mx);
+                        }
+                        sum64 = warp_sum(sum64);
+                    }
+                    for (int c = lane; c < C; c += 32) {
+                        const int e = (int32_t)~(uint32_t)s.key[c];
+                        const double v = gate_logit(p, t, e);
+                        s.exact[c] = (p.sigmoid ? 1.0 / (1.0 + exp(-v)) : exp(v - (double)mx) / sum64) + (double)p.bias[e];
+                    }
+                    __syncwarp();
+                    for (int c = lane; c < C; c += 32) {
+                        const double v = s.exact[c];
+                        const uint32_t low = (uint32_t)s.key[c];  // larger: lower id
+                        int place = 0;
+                        for (int j = 0; j < C; ++j)
+                            place += s.exact[j] > v || (s.exact[j] == v && (uint32_t)s.key[j] > low) ? 1 : 0;
+                        if (place < p.k) s.id[place] = (int32_t)~low;
+                    }
+                    __syncwarp();
+                }
+            }
+            int mine = -1;
+            float w = 0.f;
+            if (lane < got) {
+                mine = s.id[lane];
+                const float v = BIAS ? gate_logit(p, t, mine) : s.sorted[lane];
+                if (p.sigmoid) {
+                    w = 1.0f / (1.0f + expf(-v));
+                } else {
+                    const float d = v - mx, y = d - v, x = (v - (d - y)) - (mx + y);  // d + x = v - mx exactly
+                    w = d < -100.f ? 0.f : expf(d) * (1.0f + x) / sum;
+                }
+            }
+            if (__any_sync(all, mine >= 0 && w < 0x1p-100f)) {
+                unsettled = true;
+            } else {
+                float z = w;
+                for (int q = 16; q > 0; q >>= 1) z += __shfl_xor_sync(all, z, q);
+                if (lane < p.k) {
+                    p.idx[t * p.k + lane] = mine;
+                    p.weight[t * p.k + lane] = (p.renorm ? (z == 0.f ? 0.f : w / z) : w) * p.scale;
+                }
+            }
+        }
+    }
+    if (__syncthreads_or(unsettled)) {
+        for (int w = 0; w < kGateWarps; ++w) {
+            if (w == warp && unsettled) gate_exact(p, t, slow);
+            __syncthreads();
+        }
     }
 }
 

@@ -835,6 +835,27 @@ k3moe_status check_linear(const k3moe_linear_desc *l) {
     return K3MOE_OK;
 }
 
+// A warp per token, the logits of a lane in 4 * ceil(E / 128) registers.
+template <int NI>
+cudaError_t launch_gate_ni(const GateParams &p, cudaStream_t st) {
+    const dim3 grid((unsigned)ceil_div(p.T, kGateWarps)), block(32 * kGateWarps);
+    const size_t smem = gate_smem(p.E, p.groups);
+    return p.bias ? launch(gate_kernel<NI, true>, grid, block, smem, st, true, p)
+                  : launch(gate_kernel<NI, false>, grid, block, smem, st, true, p);
+}
+cudaError_t launch_gate(const GateParams &p, cudaStream_t st) {
+    switch (ceil_div(p.E, 128)) {
+        case 1: return launch_gate_ni<1>(p, st);
+        case 2: return launch_gate_ni<2>(p, st);
+        case 3: return launch_gate_ni<3>(p, st);
+        case 4: return launch_gate_ni<4>(p, st);
+        case 5: return launch_gate_ni<5>(p, st);
+        case 6: return launch_gate_ni<6>(p, st);
+        case 7: return launch_gate_ni<7>(p, st);
+        default: return launch_gate_ni<8>(p, st);
+    }
+}
+
 // Launch with programmatic stream serialisation in clusters of n CTAs.
 template <typename Kern, typename P>
 cudaError_t launch_cluster(Kern kernel, int grid, int block, size_t smem, int n, cudaStream_t s, const P &params) {
@@ -1366,8 +1387,8 @@ k3moe_status k3moe_gate(const void *logits, int64_t ld, int32_t T, const float *
     p.scale = gate->weight_scale;
     p.idx = idx;
     p.weight = weight;
-    cudaError_t e = launch(gate_kernel, dim3(T < 65536 ? T : 65536), dim3(32), 0, reinterpret_cast<cudaStream_t>(stream),
-                           false, p);
+    p.vec = ld % 4 == 0 && aligned(logits, bf16 ? 8 : 16) && (!bias || aligned(bias, 16));
+    cudaError_t e = launch_gate(p, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? K3MOE_OK : cuda_fail(e, "gate launch");
 }
 
