@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libk3moe.so")
@@ -242,41 +243,38 @@ def k3moe_layer_timed(x, T, w_router, bias, expert_blobs, shared_wg, shared_wu, 
     return st, nk.value
 
 
-def _rows(t, sizes, cols):
-    """Row distance of a 2-D operand given as a tensor (0: rows without gaps);
-    -1, which the library refuses, when the tensor is not `cols` wide with
-    consecutive elements of one of the given sizes in bytes."""
-    if t is None or isinstance(t, int):
-        return 0
-    if t.element_size() not in sizes or t.shape[-1] != cols or (cols > 1 and t.stride(-1) != 1):
-        return -1
-    if t.dim() == 1 or t.shape[0] == 1:
-        return cols if t.dim() < 3 else -1
-    return t.stride(0) if t.dim() == 2 and t.stride(0) >= cols else -1
+def _load_binding():
+    """The compiled entry points of the calls below (csrc/py_binding.cpp): they
+    read the tensors' addresses and strides themselves.  Needs torch."""
+    global _binding
+    import torch  # noqa: F401  (its libraries, before the module that links them)
+    path = os.path.join(_PKG, "_binding.so")
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is missing: build it with "
+                          "`python mxfp4_routed_expert_softmax_b200/build.py`")
+    import importlib.util
+    spec = importlib.util.spec_from_file_location("_binding", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    mod.bind(*(ctypes.cast(f, _vp).value for f in (lib.k3moe_gate, lib.k3moe_linear, lib.k3moe_layer_routed)))
+    _binding = mod
+    return mod
 
 
-def _flat(*ts) -> bool:
-    """Whether every tensor given is contiguous and of 4-byte elements."""
-    return all(t is None or isinstance(t, int) or (t.element_size() == 4 and t.is_contiguous()) for t in ts)
+_binding = None
+if "torch" in sys.modules:
+    _load_binding()
 
 
 def k3moe_gate(logits, T, bias, gate, idx, weight, stream=None) -> int:
     """logits: [T, E] tensor (rows may be a slice of wider ones) or an address."""
-    ld = _rows(logits, (2,) if gate.flags & K3MOE_LOGITS_BF16 else (4,), gate.n_experts)
-    if ld < 0 or not _flat(bias, idx, weight):
-        return K3MOE_ERR_INVALID_ARGUMENT
-    return lib.k3moe_gate(_ptr(logits), ld, T, _ptr(bias), ctypes.byref(gate), _ptr(idx), _ptr(weight),
-                          _stream(stream))
+    return (_binding or _load_binding()).gate(logits, T, bias, gate, idx, weight, stream)
 
 
 def k3moe_layer_routed(x, T, idx, weight, expert_blobs, shared_wg, shared_wu, shared_wd, dims, y, ws,
                        ws_bytes=None, stream=None) -> int:
-    if not _flat(idx, weight):
-        return K3MOE_ERR_INVALID_ARGUMENT
-    ws_bytes = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
-    return lib.k3moe_layer_routed(_ptr(x), T, _ptr(idx), _ptr(weight), _ptr(expert_blobs), _ptr(shared_wg),
-                                  _ptr(shared_wu), _ptr(shared_wd), ctypes.byref(dims), _ptr(y), _ptr(ws), ws_bytes,
-                                  _stream(stream))
+    return (_binding or _load_binding()).layer_routed(x, T, idx, weight, expert_blobs, shared_wg, shared_wu, shared_wd,
+                                                      dims, y, ws, ws_bytes, stream)
 
 
 def k3moe_linear_workspace_size(lin: k3moe_linear_desc, T_max: int) -> int:
@@ -285,14 +283,7 @@ def k3moe_linear_workspace_size(lin: k3moe_linear_desc, T_max: int) -> int:
 
 def k3moe_linear(x, T, w, w_gate, bias, bias_gate, residual, lin, out, ws, ws_bytes=None, stream=None) -> int:
     """Tensors (x, w, w_gate, residual, out) may be slices of wider rows."""
-    osz = (4,) if lin.flags & K3MOE_OUT_FP32 else (2,)
-    ldx, ldw, ldr, ldo = _rows(x, (2,), lin.k), _rows(w, (2,), lin.k), _rows(residual, osz, lin.n), _rows(out, osz, lin.n)
-    if min(ldx, ldw, ldr, ldo) < 0 or not _flat(bias, bias_gate) or (w_gate is not None
-                                                                    and _rows(w_gate, (2,), lin.k) != ldw):
-        return K3MOE_ERR_INVALID_ARGUMENT
-    ws_bytes = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
-    return lib.k3moe_linear(_ptr(x), ldx, T, _ptr(w), _ptr(w_gate), ldw, _ptr(bias), _ptr(bias_gate), _ptr(residual),
-                            ldr, ctypes.byref(lin), _ptr(out), ldo, _ptr(ws), ws_bytes, _stream(stream))
+    return (_binding or _load_binding()).linear(x, T, w, w_gate, bias, bias_gate, residual, lin, out, ws, ws_bytes, stream)
 
 
 def new_linear_workspace(lin: k3moe_linear_desc, T_max: int, device="cuda"):

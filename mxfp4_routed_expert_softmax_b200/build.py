@@ -1,4 +1,5 @@
-"""Build libk3moe.so in-tree with nvcc for sm_100a.
+"""Build libk3moe.so in-tree with nvcc for sm_100a, and _binding.so, the Python
+entry points of the shortest calls, with the host compiler.
 
 Run as a script (``python mxfp4_routed_expert_softmax_b200/build.py``): the
 package itself refuses to import until the library exists."""
@@ -14,6 +15,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libk3moe.so")
+BINDING = os.path.join(PKG, "_binding.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
@@ -25,23 +27,46 @@ def sources():
                   + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
+def binding_sources():
+    return [os.path.join(CSRC, "py_binding.cpp"), os.path.join(INCLUDE, "k3moe.h")]
+
+
+def _older(out: str, srcs) -> bool:
+    return not os.path.exists(out) or any(os.path.getmtime(s) > os.path.getmtime(out) for s in srcs)
+
+
 def stale() -> bool:
-    if not os.path.exists(LIB):
-        return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(s) > t for s in sources())
+    return _older(LIB, sources()) or _older(BINDING, binding_sources())
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile the library if it is missing or older than its sources."""
-    if not force and not stale():
-        return LIB
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [NVCC, *FLAGS, "-I", INCLUDE, "-o", tmp, os.path.join(CSRC, "k3moe_api.cu")]
+def _compile(cmd, out: str, verbose: bool) -> None:
+    tmp = out + f".tmp{os.getpid()}"
+    cmd = [*cmd, "-o", tmp]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.check_call(cmd)
-    os.replace(tmp, LIB)
+    os.replace(tmp, out)
+
+
+def _binding_command():
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++20", "-fPIC", "-shared", "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"]]
+    for p in include_paths("cuda"):
+        cmd += ["-isystem", p]
+    return cmd + [binding_sources()[0], "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Compile what is missing or older than its sources."""
+    if force or _older(LIB, sources()):
+        _compile([NVCC, *FLAGS, "-I", INCLUDE, os.path.join(CSRC, "k3moe_api.cu")], LIB, verbose)
+    if force or _older(BINDING, binding_sources()):
+        _compile(_binding_command(), BINDING, verbose)
     return LIB
 
 
