@@ -308,8 +308,8 @@ __global__ void pf_items_kernel(const __grid_constant__ PfRouteParams p) {
 // x as kPfPieces E2M1 pieces, written straight into the B tile of every group
 // that has the token (the gate/up MMA's layout: chunk c of B row 4s + piece
 // at c*(kPfN/8)*128 + (row/8)*128 + (row%8)*16, scale words [2][kPfN]).  One
-// warp per (token, K-tile): the 8 blocks of 32 are quantised into a
-// shared-memory staging block, then lane 4c + piece holds chunk c's 16 bytes
+// warp per (token, K-tile): the 8 blocks of 32 are quantised (a half block per
+// lane) into a shared-memory staging block, then lane 4c + piece holds chunk c's 16 bytes
 // of that piece and stores them for each of the token's k groups.  With a
 // shared expert, x also goes as bf16 into the shared groups' tiles (MMA N =
 // 32 rows, one per token; rows of absent tokens zero).
@@ -329,19 +329,40 @@ __global__ void __launch_bounds__(kRouteThreads) pf_prep_kernel(const __grid_con
         const int t = i / nkt, kt = i - t * nkt;
         const bool real = t < p.T;
         const int nbk = min(8, nb - kt * 8);  // 32-blocks in this K-tile
-        if (lane < 8) *reinterpret_cast<uint32_t *>(&sstage[wl][lane >> 2][lane & 3][0]) = 0u;
-        __syncwarp();
-        for (int c = 0; c < nbk; ++c) {
-            const int col = 32 * (kt * 8 + c) + lane;
-            const uint16_t xv = real ? p.r.x[(size_t)t * d + col] : (uint16_t)0;
-            if (real)
-                quantize_pieces_t<kPfPieces>(__uint_as_float((uint32_t)xv << 16), lane, 0, c, kPfPieces * 16, 0,
-                                             kPfPieces, &stage[wl][0][0][0], &sstage[wl][0][0][0]);
-            if (p.ngs > 0) {
-                const int gs = t / kGroup, j = t - gs * kGroup;
+        // lanes c and c + 16 (c < 8) quantise the halves of the K-tile's block c
+        const int c0 = lane & 15, half = lane >> 4;
+        const bool in = real && c0 < nbk;  // 16 columns of this lane
+        uint4 xw[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+        if (in) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(p.r.x + (size_t)t * d + 32 * (kt * 8 + c0) + 16 * half);
+            xw[0] = src[0];
+            xw[1] = src[1];
+        }
+        float r[16];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t w[4] = {xw[h].x, xw[h].y, xw[h].z, xw[h].w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) r[8 * h + 2 * q] = bf16_lo(w[q]), r[8 * h + 2 * q + 1] = bf16_hi(w[q]);
+        }
+        uint2 code[kPfPieces];
+        uint32_t exps;
+        quantize_pieces_half<kPfPieces>(r, code, exps);
+        if (c0 < 8) {
+#pragma unroll
+            for (int pc = 0; pc < kPfPieces; ++pc) {
+                *reinterpret_cast<uint2 *>(&stage[wl][c0][pc][8 * half]) = code[pc];
+                if (half == 0) sstage[wl][c0 >> 2][pc][c0 & 3] = c0 < nbk ? (uint8_t)(exps >> (8 * pc)) : (uint8_t)0;
+            }
+        }
+        if (p.ngs > 0 && c0 < nbk) {
+            const int gs = t / kGroup, j = t - gs * kGroup;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int col = 32 * (kt * 8 + c0) + 16 * half + 8 * h;
                 uint8_t *tile = ws + p.P.xbf + ((size_t)gs * nkts + col / kTileKs) * kPfNsGU * 128;
-                const int cc = (col % kTileKs) / 8, e = col % 8;
-                *reinterpret_cast<uint16_t *>(tile + cc * (kPfNsGU / 8) * 128 + (j / 8) * 128 + (j % 8) * 16 + e * 2) = xv;
+                const int cc = (col % kTileKs) / 8;
+                *reinterpret_cast<uint4 *>(tile + cc * (kPfNsGU / 8) * 128 + (j / 8) * 128 + (j % 8) * 16) = xw[h];
             }
         }
         if (!real) continue;

@@ -41,6 +41,8 @@ struct PfUmmaParams {
     int strict;        // flag E8M0 NaN bytes (0xFF) among the weight scales read
 };
 
+constexpr int kPfHx = 33;  // floats from token to token where h changes from a row to a token per lane
+
 struct PfSlot {
     int32_t eid;         // expert (-1: shared)
     int32_t g;           // group index (shared: routed groups + s)
@@ -61,7 +63,7 @@ __host__ __device__ inline int pf_sfa_off(bool gu) { return (gu ? 2 : 1) * kAtil
 __host__ __device__ inline int pf_sfb_off(bool gu) { return pf_sfa_off(gu) + (gu ? 2 : 1) * 2048; }
 __host__ __device__ inline int pf_stage_bytes(bool gu) { return (pf_sfb_off(gu) + 2 * kPfN * 4 + 1023) & ~1023; }
 __host__ __device__ inline int pf_smem_bytes(bool gu, int nst) {
-    return 1024 + nst * pf_stage_bytes(gu) + 512 + kPfSlots * (int)sizeof(PfSlot);
+    return 1024 + nst * pf_stage_bytes(gu) + 512 + kPfSlots * (int)sizeof(PfSlot) + (gu ? 4 * 16 * kPfHx * 4 : 0);
 }
 
 template <bool GU>
@@ -427,6 +429,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) pf_expert_kernel(const __grid_c
         // --------------------------------------------------- epilogue --
         const uint32_t lb = umma::lane_base(warp);
         const int rowl = 32 * warp + lane;
+        float *hx = reinterpret_cast<float *>(slots + kPfSlots) + warp * 16 * kPfHx;  // gate/up only
         for (int q = 0; q < nmine; ++q) {
             const PfSlot *sl = slot_wait(q);
             if (!sl) break;
@@ -484,18 +487,35 @@ __global__ void __launch_bounds__(kPfThreads, 1) pf_expert_kernel(const __grid_c
                         const size_t tb = (size_t)sl->g * nkt_ff + (blk >> 3);
                         uint8_t *tile = p.ws + p.P.hb + tb * kPfN * 128;
                         uint8_t *sfw = p.ws + p.P.hsf + tb * 2 * kPfN * 4;
-                        // 4 tokens at a time (absent tokens' rows get zeros; nothing reads them)
+                        // 16 tokens at a time through shared memory: lanes j and
+                        // j + 16 then hold the two halves of token j's block
+                        // (absent tokens' rows get zeros; nothing reads them)
+                        const int j = lane & 15, half = lane >> 4, c = blk & 7;
 #pragma unroll
-                        for (int j0 = 0; j0 < kGroup; j0 += 4) {
-                            if (j0 < n) {
-                                float h[4];
+                        for (int t0 = 0; t0 < kGroup; t0 += 16) {
+                            if (t0 < n) {
 #pragma unroll
-                                for (int b = 0; b < 4; ++b) {
-                                    const int j = j0 + b;
-                                    h[b] = (ok && f < p.ff && j < n) ? silu_mul(acc[0][j], acc[1][j]) * sl->w[j] : 0.f;
+                                for (int i = 0; i < 16; ++i) {
+                                    const int t = t0 + i;
+                                    hx[i * kPfHx + lane] =
+                                        (ok && f < p.ff && t < n) ? silu_mul(acc[0][t], acc[1][t]) * sl->w[t] : 0.f;
                                 }
-                                quantize_pieces_batch<kPfPieces, 4>(h, lane, j0, blk & 7, (kPfN / 8) * 128, 128, kPfN,
-                                                                    tile, sfw);
+                                __syncwarp();
+                                float r[16];
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) r[i] = hx[j * kPfHx + 16 * half + i];
+                                uint2 code[kPfPieces];
+                                uint32_t exps;
+                                quantize_pieces_half<kPfPieces>(r, code, exps);
+                                const int row0 = (t0 + j) * kPfPieces;  // B rows of the token's pieces
+                                uint8_t *dst = tile + c * (kPfN / 8) * 128 + (row0 / 8) * 128 + (row0 % 8) * 16 + 8 * half;
+#pragma unroll
+                                for (int pc = 0; pc < kPfPieces; ++pc) {
+                                    *reinterpret_cast<uint2 *>(dst + pc * 16) = code[pc];
+                                    if (half == 0)
+                                        sfw[((c >> 2) * kPfN + row0 + pc) * 4 + (c & 3)] = (uint8_t)(exps >> (8 * pc));
+                                }
+                                __syncwarp();
                             }
                         }
                     } else if (f < p.ffs) {
