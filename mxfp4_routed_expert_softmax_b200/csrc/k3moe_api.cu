@@ -89,6 +89,16 @@ cudaError_t max_clusters(Kern kernel, int n, int threads, int *out) {
     return cudaOccupancyMaxActiveClusters(out, kernel, &cfg);
 }
 
+using LinearTileKernel = void (*)(const LinearTcParams);
+template <bool GATED>
+LinearTileKernel linear_tile_of(bool resid, bool fp32) {
+    return resid ? (fp32 ? linear_tile_kernel<GATED, true, true> : linear_tile_kernel<GATED, true, false>)
+                 : (fp32 ? linear_tile_kernel<GATED, false, true> : linear_tile_kernel<GATED, false, false>);
+}
+LinearTileKernel linear_tile_variant(bool gated, bool resid, bool fp32) {
+    return gated ? linear_tile_of<true>(resid, fp32) : linear_tile_of<false>(resid, fp32);
+}
+
 // One-time per-device set-up: SM count and the shared-memory opt-ins.
 k3moe_status device_info(DeviceInfo **out) {
     int dev = 0;
@@ -108,13 +118,13 @@ k3moe_status device_info(DeviceInfo **out) {
         if (r == cudaSuccess) r = set_smem(layer_kernel<1, true>, big);
         if (r == cudaSuccess) r = set_smem(layer_kernel<0, false>, big);
         if (r == cudaSuccess) r = set_smem(pf_router_mma_kernel, rm_smem_bytes());
-        if (r == cudaSuccess) r = set_smem(linear_tile_kernel, big);
+        for (int i = 0; i < 8 && r == cudaSuccess; ++i) r = set_smem(linear_tile_variant(i & 1, i & 2, i & 4), big);
         if (r == cudaSuccess) r = set_smem(linear_pair_kernel<false, false>, big);
         if (r == cudaSuccess) r = set_smem(linear_pair_kernel<false, true>, big);
         if (r == cudaSuccess) r = set_smem(linear_pair_kernel<true, false>, big);
         if (r == cudaSuccess) r = set_smem(linear_pair_kernel<true, true>, big);
         for (int s = 2; s <= kLtMaxSplit && r == cudaSuccess; ++s)
-            r = max_clusters(linear_tile_kernel, s, kLtThreads, &di.clusters[s]);
+            r = max_clusters(linear_tile_variant(true, true, false), s, kLtThreads, &di.clusters[s]);
         if (r == cudaSuccess) r = max_clusters(linear_pair_kernel<true, true>, 2, kLpThreads, &di.pairs);
         if (r != cudaSuccess) return cuda_fail(r);
         di.ready = true;
@@ -973,16 +983,17 @@ k3moe_status linear_launch(const LinearParams &p, WsHeader *hdr, cudaStream_t st
     const int steps = ceil_div(nkt, a.split);
     a.chain = std::min(chain, steps);
     const bool chains = steps > a.chain;
-    // one CTA and one chain: the reduction buffer lies over the finished stages
-    const bool apart = a.split > 1 || chains;
-    const int red = (a.split * ceil_div(a.bn, a.split) + (a.split > 1 && chains ? a.bn : 0)) * 512;
-    a.nst = std::min((room - (apart ? red : 0)) / sb, kLtMaxStages);
-    if (apart) a.nst = std::min(a.nst, steps);
-    a.red = kLtHead + (apart ? a.nst * sb : 0);
+    // one chain: a CTA's own sums lie over its finished stages
+    const int red = a.split > 1 ? a.split * ceil_div(a.bn, a.split) * 512 : 0, part = a.bn * 512;
+    a.nst = std::min({(room - red - (chains ? part : 0)) / sb, kLtMaxStages, std::max(steps, 2)});
+    const int stages = std::max(a.nst * sb, chains ? 0 : part);
+    a.part = kLtHead + (chains ? stages : 0);
+    a.red = kLtHead + stages + (chains ? part : 0);
     a.tcols = 32;
     while (a.tcols < (chains ? 2 : 1) * a.bn) a.tcols *= 2;
-    const int bytes = 1024 + kLtHead + a.nst * sb + (apart ? red : 0);
-    e = launch_cluster(linear_tile_kernel, a.nrb * a.ntt * a.split, kLtThreads, bytes, a.split, st, a);
+    const int bytes = 1024 + a.red + red;
+    e = launch_cluster(linear_tile_variant(gated, p.resid != nullptr, p.out_fp32 != 0), a.nrb * a.ntt * a.split, kLtThreads,
+                       bytes, a.split, st, a);
     return e == cudaSuccess ? K3MOE_OK : cuda_fail(e, "linear launch");
 }
 

@@ -29,7 +29,7 @@ __device__ __forceinline__ void linear_act(float (&v)[NV], int act) {
         for (int i = 0; i < NV; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];  // NaN stays NaN
     } else if (act == K3MOE_ACT_SILU) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) v[i] = v[i] / (1.0f + expf(-v[i]));
+        for (int i = 0; i < NV; ++i) v[i] = __fdividef(v[i], 1.0f + __expf(-v[i]));  // within 4 units in the last place + |v| 2^-24
     } else if (act == K3MOE_ACT_GELU) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) v[i] = 0.5f * v[i] * erfcf(-0.70710678118654752f * v[i]);
@@ -43,8 +43,8 @@ __device__ __forceinline__ void linear_act(float (&v)[NV], int act) {
 __device__ __forceinline__ uint16_t bf16_bits(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
 
 // The epilogues finish NV neighbouring columns of one token in a thread: one
-// 16-byte access to the residual and to the output (bf16, NV = 8) where their
-// rows allow it.  (One column per lane, 2-byte accesses: the down projection
+// access of 8 or 16 bytes to the residual and to the output (bf16, NV = 4 or
+// 8) where their rows allow it.  (One column per lane, 2-byte accesses: the down projection
 // of 4095 tokens took 114 us.)
 template <int NV>
 struct Residual {
@@ -72,6 +72,9 @@ __device__ __forceinline__ void linear_resid(const LinearParams &p, long long t,
         if (NV == 8 && p.vec && n + NV <= p.N) {
             const uint4 v = *reinterpret_cast<const uint4 *>(q);
             r.w[0] = v.x, r.w[1 % NV] = v.y, r.w[2 % NV] = v.z, r.w[3 % NV] = v.w;
+        } else if (NV == 4 && p.vec && n + NV <= p.N) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(q);
+            r.w[0] = v.x, r.w[1 % NV] = v.y;
         } else {
             uint16_t h[NV];
 #pragma unroll
@@ -124,11 +127,13 @@ __device__ __forceinline__ void linear_finish(const LinearParams &p, long long t
         uint16_t h[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) h[i] = bf16_bits(v[i]);
-        if (NV == 8 && p.vec && n + NV <= p.N) {
-            uint32_t w[4];
+        uint32_t w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = h[2 * i % NV] | (uint32_t)h[(2 * i + 1) % NV] << 16;
+        for (int i = 0; i < 4; ++i) w[i] = h[2 * i % NV] | (uint32_t)h[(2 * i + 1) % NV] << 16;
+        if (NV == 8 && p.vec && n + NV <= p.N) {
             *reinterpret_cast<uint4 *>(q) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else if (NV == 4 && p.vec && n + NV <= p.N) {
+            *reinterpret_cast<uint2 *>(q) = make_uint2(w[0], w[1]);
         } else {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
@@ -269,7 +274,8 @@ __global__ void __launch_bounds__(512, 1) linear_stream_kernel(const __grid_cons
 // token at once, whatever the rows' alignment, and a column's bias is one
 // register.  A gated product stacks 64 rows of w and 64 of w_gate into the 128
 // rows; the two are brought together through shared memory in the epilogue.
-constexpr int kLtThreads = 320;  // warps 0-7 epilogue (two per lane quadrant), 8 copies, 9 MMA issue
+constexpr int kLtEpi = 16;                     // epilogue warps: four per lane quadrant
+constexpr int kLtThreads = 32 * (kLtEpi + 2);  // and one that copies, one that issues MMAs
 constexpr int kLtKStep = 64;     // bf16 per K-step: 128 bytes of every row, one swizzle atom
 constexpr int kLtA = 128 * 128;  // bytes of the weight box per stage
 constexpr int kLtHead = 1024;    // barriers, before the stages
@@ -289,7 +295,7 @@ struct LinearTcParams {
     int split;       // tile kernel: CTAs (one cluster) that share a tile's K
     int chain;       // tile kernel: K-steps accumulated in tensor memory at a stretch
     int tcols;       // tensor-memory columns
-    int red;         // tile kernel: offset of the reduction buffer
+    int part, red;   // tile kernel: offsets of its own sums and of the other CTAs' parts
     WsHeader *hdr;
     uint64_t wait_ns;
 };
@@ -298,14 +304,16 @@ __device__ __forceinline__ void prefetch_tmap(const void *m) { asm volatile("pre
 
 // A tile of 128 weight rows x bn tokens per cluster of `split` CTAs, which
 // share its K: each accumulates its part, sends every CTA of the cluster the
-// columns that CTA finishes (over distributed shared memory), and finishes its
-// own columns, adding the parts in rank order.
+// columns that CTA finishes (one bulk copy each over distributed shared
+// memory; stores of single values took 1.8 us for 112 columns), and finishes
+// its own columns, adding the parts in rank order.
 //
 // The tensor core cuts its running sum at every step, so a long chain drifts:
 // with fp32 outputs the sum moves to shared memory every `chain` K-steps (two
 // tensor-memory buffers) and the pieces are added there, rounded to nearest;
 // bf16 outputs take one chain, whose drift (2^-24 a step of 16) is far below
 // the output's half step of 2^-9.
+template <bool GATED, bool RESID, bool OUT32>
 __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid_constant__ LinearTcParams a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -317,11 +325,11 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
     uint64_t *afull = empty + nst;
     uint64_t *aempty = afull + 2;
     uint64_t *mdone = aempty + 2;
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(mdone + 1);
+    uint64_t *rfull = mdone + 1;  // the other CTAs' parts of this CTA's columns have arrived
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(rfull + 1);
     volatile int *s_abort = reinterpret_cast<volatile int *>(tslot + 1);
     uint8_t *stages = smem + kLtHead;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (S > 1) umma::cluster_arrive();  // "this CTA has started": a remote write needs it
     if (threadIdx.x == 0) {
         for (int s = 0; s < nst; ++s) {
             mbar_init(&full[s], 1);
@@ -329,26 +337,29 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&afull[b], 1);
-            mbar_init(&aempty[b], 8);
+            mbar_init(&aempty[b], kLtEpi);
         }
         mbar_init(mdone, 1);
+        mbar_init(rfull, 1);
         fence_mbar_init();
         *s_abort = 0;
     }
-    if (warp == 8 && lane == 0) {
+    if (warp == kLtEpi && lane == 0) {
         prefetch_tmap(a.tw);
         prefetch_tmap(a.tx);
     }
     if (warp == 0) umma::tmem_alloc(tslot, (uint32_t)a.tcols);
     umma::fence_before();
     __syncthreads();
-    if (S > 1) umma::cluster_wait();
+    if (S > 1) {  // the barriers of every CTA of the cluster are set up
+        umma::cluster_arrive();
+        umma::cluster_wait();
+    }
     umma::fence_after();
     const uint32_t tbase = *tslot;
     const int rank = S > 1 ? (int)umma::cluster_rank() : 0;
     const int tile = blockIdx.x / S;
-    const bool gated = p.wg != nullptr;
-    const int nrow = gated ? 64 : 128;
+    const int nrow = GATED ? 64 : 128;
     const int n0 = (tile % a.nrb) * nrow, t0 = (tile / a.nrb) * bn;
     const int nkt = ceil_div(p.K, kLtKStep);
     const int kt0 = (int)((long long)nkt * rank / S), nk = (int)((long long)nkt * (rank + 1) / S) - kt0;
@@ -358,25 +369,14 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
     pdl_wait();
     pdl_trigger();
 
-    const int half = warp >> 2, hcols = ((bn / 16 + 1) / 2) * 16;  // columns of the first of a quadrant's warps
-    const int c0 = half * hcols, ncol = half ? bn - hcols : hcols;
-    // What a thread finishes: 8 rows (output columns n..n+7) of the tokens
-    // j0, j0 + step, ... of this CTA, NU at a time.  The first residuals are
-    // loaded before the sums are waited for.
-    constexpr int NU = 4;
-    const int rowg = nrow / 8, n = n0 + (threadIdx.x % rowg) * 8, j0 = threadIdx.x / rowg, step = 256 / rowg;
-    const int jmax = n < p.N && warp < 8 ? min(cpo, min(bn, p.T - t0) - rank * cpo) : 0;
-    Residual<8> res[NU];
-    auto fetch = [&](int j) {
-#pragma unroll
-        for (int i = 0; i < NU; ++i)
-            if (j0 + (j + i) * step < jmax) linear_resid(p, (long long)t0 + rank * cpo + j0 + (j + i) * step, n, res[i], p.out_fp32);
-    };
-    // red[source][column][row]: the columns this CTA finishes; sum[column][row]:
-    // this CTA's sums of the chains before the last (one CTA: the same buffer)
+    // part[column][row]: this CTA's sums (of the chains so far); red[source][
+    // column][row]: the other CTAs' parts of the columns this CTA finishes.
+    float *part = reinterpret_cast<float *>(smem + a.part);
     float *red = reinterpret_cast<float *>(smem + a.red);
-    float *sum = S > 1 ? red + S * cpo * 128 : red;
-    if (warp == 8) {
+    const int cend = min(bn, p.T - t0);                     // columns that exist
+    const int jmax = max(0, min(cpo, cend - rank * cpo));   // of them, finished here
+    if (S > 1 && threadIdx.x == 0 && jmax > 0) mbar_arrive_expect_tx(rfull, (uint32_t)((S - 1) * jmax * 512));
+    if (warp == kLtEpi) {
         int i = 0, s = 0;
         uint32_t ph = 1u;  // of the empty barriers: the first round's waits pass at once
         for (; i < nk; ++i) {
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
                 const int x = (kt0 + i) * kLtKStep;
                 mbar_arrive_expect_tx(&full[s], (uint32_t)SB);
                 umma::tma_load_2d(st, a.tw, x, n0, &full[s]);
-                if (gated) umma::tma_load_2d(st + kLtA / 2, a.twg, x, n0, &full[s]);
+                if (GATED) umma::tma_load_2d(st + kLtA / 2, a.twg, x, n0, &full[s]);
                 umma::tma_load_2d(st + kLtA, a.tx, x, t0, &full[s]);
             }
             __syncwarp();
@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
                 mbar_drain(&full[t], (uint32_t)((last / nst) & 1), a.wait_ns);
             }
         }
-    } else if (warp == 9) {
+    } else if (warp == kLtEpi + 1) {
         const uint64_t adesc = umma::smem_desc(smem_u32(stages), 16u, 1024u, umma::kLayoutSw128);
         const uint32_t idesc = umma::idesc_bf16(bn);
         int i = 0, s = 0;
@@ -440,84 +440,80 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
             mbar_drain(mdone, 0u, a.wait_ns);
         }
     } else {
-        fetch(0);
+        // A thread finishes 4 columns of the tokens j0, j0 + step, ... of its
+        // CTA's (a warp's lanes: one token, or two of a gated product); the
+        // biases and the first residual are loaded while the MMAs run.
+        constexpr int lpt = GATED ? 16 : 32, step = kLtEpi * 32 / lpt;
+        const int n = n0 + lane % lpt * 4, j0 = threadIdx.x / lpt;
+        const long long tq = (long long)t0 + rank * cpo;
+        float b[4], bg[4];
+        Residual<4> res;
+        linear_bias(p.bias, n, p.N, b);
+        linear_bias(p.bias_g, n, p.N, bg);
+        if (RESID && n < p.N && j0 < jmax) linear_resid(p, tq + j0, n, res, OUT32);
+        __syncwarp();
         for (int c = 0; c < nch; ++c) {
             const int buf = c & 1;
             if (!wait(&afull[buf], (uint32_t)((c >> 1) & 1))) break;
             umma::fence_after();
-            const uint32_t src = tbase + umma::lane_base(warp) + (uint32_t)(buf * bn + c0);
-            const bool last = c == nch - 1;
-            int o = c0 / cpo, jo = c0 - o * cpo;  // where column c0 goes: CTA o's column jo
-            const int row = 32 * (warp & 3) + lane, cend = min(c0 + ncol, p.T - t0);
-            const uint32_t mine = smem_u32(red) + (uint32_t)(rank * cpo * 128 + row) * 4u;
-            for (int j = c0; j < cend; j += 16) {
+            const uint32_t src = tbase + umma::lane_base(warp) + (uint32_t)(buf * bn);
+            float *dst = part + 32 * (warp & 3) + lane;
+            for (int j = 16 * (warp >> 2); j < cend; j += 4 * kLtEpi) {
                 uint32_t r[16];
-                float v[16];
-                umma::ld16(src + (j - c0), r);
+                umma::ld16(src + j, r);
                 umma::wait_ld();
-                float *sj = sum + j * 128 + row;
+                float *d = dst + j * 128;
+                if (c == 0) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-                if (c > 0) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] += sj[i * 128];
-                }
-                if (!last || S == 1) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) sj[i * 128] = v[i];
+                    for (int i = 0; i < 16; ++i) d[i * 128] = __uint_as_float(r[i]);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        if (j + i < cend) umma::st_cluster(umma::mapa(mine + (uint32_t)jo * 512u, (uint32_t)o), v[i]);
-                        if (++jo == cpo) {
-                            jo = 0;
-                            ++o;
-                        }
-                    }
+                    for (int i = 0; i < 16; ++i) d[i * 128] += __uint_as_float(r[i]);
                 }
             }
             umma::fence_before();
             __syncwarp();
             if (lane == 0)
                 asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&aempty[buf])) : "memory");
+            __syncwarp();
+        }
+        if (S > 1) fence_proxy_async();  // the copies below read what was stored here
+        umma::bar_sync(1, 32 * kLtEpi);
+        if (S > 1) {
+            if (threadIdx.x < S && threadIdx.x != rank) {
+                const int cols = min(cpo, cend - (int)threadIdx.x * cpo);
+                if (cols > 0)
+                    umma::bulk_s2s(umma::mapa(smem_u32(red) + (uint32_t)(rank * cpo) * 512u, threadIdx.x),
+                                   part + threadIdx.x * cpo * 128, (uint32_t)cols * 512u,
+                                   umma::mapa(smem_u32(rfull), threadIdx.x));
+            }
+            __syncwarp();
+            if (jmax > 0) wait(rfull, 0u);
+        }
+        const float *own = part + rank * cpo * 128 + (n - n0);
+        if (n < p.N) {
+            for (int j = j0; j < jmax; j += step) {
+                const Residual<4> r = res;
+                if (RESID && j + step < jmax) linear_resid(p, tq + j + step, n, res, OUT32);
+                float v[4] = {}, g[4] = {};
+                const float *src = red + j * 128 + (n - n0);
+                for (int s = 0; s < S; ++s, src += cpo * 128) {
+                    const float *q = s == rank ? own + j * 128 : src;
+                    const float4 x = *reinterpret_cast<const float4 *>(q);
+                    v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+                    if (GATED) {
+                        const float4 y = *reinterpret_cast<const float4 *>(q + 64);
+                        g[0] += y.x, g[1] += y.y, g[2] += y.z, g[3] += y.w;
+                    }
+                }
+                linear_finish(p, tq + j, n, v, g, b, bg, r, GATED, RESID, OUT32);
+            }
         }
     }
     __syncwarp();
-
-    if (S > 1) {
+    if (S > 1) {  // no CTA leaves while a copy from or into its memory may be in flight
         umma::cluster_arrive();
         umma::cluster_wait();
-    } else {
-        __syncthreads();
-    }
-    if (jmax > 0) {
-        float b[8], bg[8];
-        linear_bias(p.bias, n, p.N, b);
-        linear_bias(p.bias_g, n, p.N, bg);
-        for (int j = 0; j0 + j * step < jmax; j += NU) {
-            if (j > 0) fetch(j);
-#pragma unroll
-            for (int i = 0; i < NU; ++i) {
-                const int jj = j0 + (j + i) * step;
-                if (jj < jmax) {
-                    float v[8] = {}, g[8] = {};
-                    const float *r = red + jj * 128 + (n - n0);
-                    for (int s = 0; s < S; ++s, r += cpo * 128) {
-#pragma unroll
-                        for (int e = 0; e < 8; e += 4) {
-                            const float4 x = *reinterpret_cast<const float4 *>(r + e);
-                            v[e] += x.x, v[e + 1] += x.y, v[e + 2] += x.z, v[e + 3] += x.w;
-                            if (gated) {
-                                const float4 y = *reinterpret_cast<const float4 *>(r + 64 + e);
-                                g[e] += y.x, g[e + 1] += y.y, g[e + 2] += y.z, g[e + 3] += y.w;
-                            }
-                        }
-                    }
-                    linear_finish(p, (long long)t0 + rank * cpo + jj, n, v, g, b, bg, res[i], gated, p.resid != nullptr,
-                                  p.out_fp32);
-                }
-            }
-        }
     }
     umma::fence_before();
     __syncthreads();
@@ -698,6 +694,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid
             };
             fetch(hv * 16);
             bool got = wait(&afull[buf], (uint32_t)((q >> 1) & 1));
+            __syncwarp();
             // the two warps that exchange go on together or not at all
             if (GATED) got = umma::bar_red_and(1 + peer, 64, got);
             if (!got) break;
@@ -709,10 +706,8 @@ __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid
                 umma::wait_ld();
 #pragma unroll
                 for (int j = 0; j < 16; ++j) mine[j * kLpRow + lane] = __uint_as_float(raw[j]);
-                if (GATED)
-                    umma::bar_sync(1 + peer, 64);
-                else
-                    __syncwarp();
+                __syncwarp();
+                if (GATED) umma::bar_sync(1 + peer, 64);
                 float v[np][8], g[np][8];
 #pragma unroll
                 for (int h = 0; h < np; ++h)
@@ -731,10 +726,8 @@ __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid
                     if (f + tl + 8 * h < left)
                         linear_finish(p, (long long)t0 + f + tl + 8 * h, n, v[h], g[h], b, bg, res[h], GATED, RESID, false);
                 fetch(f + 4 * kLpEpi);
-                if (GATED)
-                    umma::bar_sync(1 + peer, 64);
-                else
-                    __syncwarp();
+                __syncwarp();
+                if (GATED) umma::bar_sync(1 + peer, 64);
             }
             umma::fence_before();
             __syncwarp();
