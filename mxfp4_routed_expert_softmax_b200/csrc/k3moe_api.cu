@@ -924,26 +924,35 @@ k3moe_status linear_launch(const LinearParams &p, WsHeader *hdr, cudaStream_t st
     a.wait_ns = wait_limit();
     const bool gated = p.wg != nullptr;
     const int nkt = ceil_div(p.K, kLtKStep);
-    // Estimated SM cycles of a K-step: the MMAs, or the operands' way from L2.
-    auto cost_tile = [&](int bn) { return std::max(2.0 * bn, (16384 + 128.0 * bn) / 48); };
-    auto cost_pair = [&](int bn) { return std::max(2.0 * bn, (16384 + 64.0 * bn) / 48); };
-    // one tile per cluster
+    // The variant of the least estimated time, in us as measured on B200.  A
+    // K-step of a tile takes what an SM takes in (64 bytes a clock) and a
+    // little; of a pair, 0.14 + 0.00094 bn (bn = 96: 0.22, 256: 0.38).  Tiles:
+    // 2 at the ends, 0.02 per column for the way out, 0.3 for a split
+    // reduction, 0.9 when the launch leaves less than half of the SMs free for
+    // the next one's start (333 x 1001 x 1000 in 112 CTAs of 48 tokens, K in
+    // two: 8.1; in 120 of 112 tokens, K in five: 9.5; 50 x 2048 x 512 in 64
+    // CTAs, K in two: 4.2; in 96, K in three: 5.1).
     const int nrb = ceil_div(p.N, gated ? 64 : 128);
-    double best = 1e300;
     const int chain = p.out_fp32 ? kLtChain : nkt;
-    for (int bm = 128; bm <= (nkt > chain ? 128 : 256); bm += 128) {
-        const int ntt = ceil_div(p.T, bm), bn = ceil_div(ceil_div(p.T, ntt), 16) * 16;
+    double best = 1e300;
+    for (int bn = 16; bn <= 256; bn += 16) {
+        const int ntt = ceil_div(p.T, bn);
+        if (bn > 16 && ceil_div(p.T, bn - 16) == ntt) continue;  // the same tiles with fewer columns
         const long long units = (long long)nrb * ntt;
-        int split = 1;
-        for (int c = 2; c <= kLtMaxSplit && bn <= 128 && 2 * c <= nkt; ++c)
-            if (units <= di->clusters[c]) split = c;
-        const double waves = (double)((units * split + di->sms - 1) / di->sms);
-        const double cost = waves * (ceil_div(nkt, split) * cost_tile(bn) + 2000 + 16 * bn);
-        if (cost < best) {
-            best = cost;
-            a.bn = bn;
-            a.ntt = ntt;
-            a.split = split;
+        for (int c = 1; c <= kLtMaxSplit && 2 * c <= std::max(nkt, 2); ++c) {
+            const int steps = ceil_div(nkt, c);
+            if (bn > 128 && (c > 1 || steps > chain)) break;
+            const int room = c > 1 ? di->clusters[c] : di->sms;  // clusters at a time
+            if (room < 1) continue;
+            const double waves = (double)((units + room - 1) / room);
+            const double step = 0.045 + (16384 + 128.0 * bn) / 121600;
+            const double cost = waves * (steps * step + 0.02 * bn) + 2 + (c > 1 ? 0.3 : 0) + (2 * units * c > di->sms ? 0.9 : 0);
+            if (cost < best) {
+                best = cost;
+                a.bn = bn;
+                a.ntt = ntt;
+                a.split = c;
+            }
         }
     }
     a.nrb = nrb;
@@ -954,7 +963,7 @@ k3moe_status linear_launch(const LinearParams &p, WsHeader *hdr, cudaStream_t st
             const int ntt = ceil_div(p.T, bn);
             const long long items = (long long)nrb2 * ntt;
             const double waves = (double)((items + di->pairs - 1) / di->pairs);
-            const double cost = waves * nkt * cost_pair(bn) + 4000 + 16 * bn;
+            const double cost = waves * (nkt * (0.14 + 0.00094 * bn) + 1.2) + 3;
             if (cost < best) {
                 best = cost;
                 pair = true;
