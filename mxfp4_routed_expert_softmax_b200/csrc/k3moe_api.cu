@@ -118,6 +118,14 @@ k3moe_status device_info(DeviceInfo **out) {
         if (r == cudaSuccess) r = set_smem(layer_kernel<1, true>, big);
         if (r == cudaSuccess) r = set_smem(layer_kernel<0, false>, big);
         if (r == cudaSuccess) r = set_smem(pf_router_mma_kernel, rm_smem_bytes());
+        if (r == cudaSuccess) r = set_smem(linear_stream_kernel<1, false, 1>, big);
+        if (r == cudaSuccess) r = set_smem(linear_stream_kernel<1, false, 2>, big);
+        if (r == cudaSuccess) r = set_smem(linear_stream_kernel<1, true, 1>, big);
+        if (r == cudaSuccess) r = set_smem(linear_stream_kernel<1, true, 2>, big);
+        if (r == cudaSuccess) r = set_smem(linear_stream_kernel<2, false, 1>, big);
+        if (r == cudaSuccess) r = set_smem(linear_stream_kernel<2, false, 2>, big);
+        if (r == cudaSuccess) r = set_smem(linear_stream_kernel<2, true, 1>, big);
+        if (r == cudaSuccess) r = set_smem(linear_stream_kernel<2, true, 2>, big);
         for (int i = 0; i < 8 && r == cudaSuccess; ++i) r = set_smem(linear_tile_variant(i & 1, i & 2, i & 4), big);
         if (r == cudaSuccess) r = set_smem(linear_pair_kernel<false, false>, big);
         if (r == cudaSuccess) r = set_smem(linear_pair_kernel<false, true>, big);
@@ -324,9 +332,9 @@ k3moe_status shared_tmaps(int d, int ffs, const void *wg, const void *wu, const 
 
 // A 2-D tensor map of 16-bit elements [rows][cols] (rows ld elements apart, 0:
 // cols), boxes of 64 columns x `box` rows with the 128-byte swizzle (the MMA's
-// K-major operand layout).
+// K-major operand layout), or of `plain` columns as they are.
 k3moe_status tmap_bf16_rows(const void *addr, int cols, int rows, uint4 (&out)[8], int64_t ld = 0,
-                            int box_rows = kRmTile) {
+                            int box_rows = kRmTile, int plain = 0) {
     std::lock_guard<std::mutex> lock(g_mu);
     static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
     if (!encode) {
@@ -343,10 +351,10 @@ k3moe_status tmap_bf16_rows(const void *addr, int cols, int rows, uint4 (&out)[8
     CUtensorMap m;
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)(ld ? ld : cols) * 2};
-    const cuuint32_t box[2] = {(cuuint32_t)kRmKStep, (cuuint32_t)box_rows};
+    const cuuint32_t box[2] = {(cuuint32_t)(plain ? plain : kRmKStep), (cuuint32_t)box_rows};
     const cuuint32_t es[2] = {1, 1};
     CUresult r = encode(&m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(addr), dims, strides, box, es,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, plain ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
         g_last_error = "cuTensorMapEncodeTiled failed (" + std::to_string((int)r) + ")";
@@ -886,38 +894,57 @@ cudaError_t launch_cluster(Kern kernel, int grid, int block, size_t smem, int n,
 }
 
 // -------------------------------------------------------- dense product --
+// Chunks of up to 256 columns, at least one per warp where K allows, and as
+// many stages as the CTAs that share an SM have room for (all of K in flight
+// up to there).
 template <int RG, bool GATED, int TG>
-cudaError_t launch_stream(const DeviceInfo &di, const LinearParams &p, cudaStream_t st) {
-    constexpr int NM = RG * (GATED ? 2 : 1), U = NM == 1 ? 8 / TG : 8 / (NM * TG) > 2 ? 8 / (NM * TG) : 2;
-    const int units = ceil_div(p.K, 64);
+k3moe_status launch_stream(const DeviceInfo &di, LinearStreamParams &a, cudaStream_t st) {
+    constexpr int NM = RG * (GATED ? 2 : 1);
+    const LinearParams &p = a.p;
     const int ctas = ceil_div(p.N, 8 * RG);
-    // 16 warps fill an SM's registers: with more CTAs than SMs, 8 each
-    const int nw = units >= 64 && ctas <= di.sms ? 16 : units >= 8 ? 8 : 4;
-    return launch(linear_stream_kernel<RG, GATED, TG, U>, dim3(ctas), dim3(32 * nw),
-                  (size_t)nw * NM * TG * 64 * 4, st, true, p);
+    const int per_sm = std::min(ceil_div(ctas, di.sms), 4);
+    for (a.kc = std::min(256, ceil_div(ceil_div(p.K, kLsWarps), 64) * 64);; a.kc -= 64) {
+        const int rounds = ceil_div(ceil_div(p.K, a.kc), kLsWarps);
+        auto fits = [&](int ns, int n) { return n * (ls_smem_bytes(NM, TG, a.kc, ns) + 1024) <= kSmemLimit + 1024; };
+        a.ns = std::min(rounds, kLsMaxStages);
+        while (a.ns > 1 && !fits(a.ns, per_sm)) --a.ns;
+        if (a.ns == 1 && rounds > 1 && fits(2, 1)) a.ns = 2;  // one CTA fewer per SM, but never a single stage
+        if (a.kc == 64 || (fits(a.ns, 1) && a.ns >= std::min(rounds, 2))) break;
+    }
+    k3moe_status s = tmap_bf16_rows(p.w, p.K, p.N, a.tw, p.ldw, 8 * RG, a.kc);
+    if (s == K3MOE_OK && GATED) s = tmap_bf16_rows(p.wg, p.K, p.N, a.twg, p.ldw, 8 * RG, a.kc);
+    if (s == K3MOE_OK) s = tmap_bf16_rows(p.x, p.K, p.T, a.tx, p.ldx, 8 * TG, a.kc);
+    if (s != K3MOE_OK) return s;
+    cudaError_t e =
+        launch(linear_stream_kernel<RG, GATED, TG>, dim3(ctas), dim3(32 * kLsWarps),
+                  (size_t)ls_smem_bytes(NM, TG, a.kc, a.ns), st, true, a);
+    return e == cudaSuccess ? K3MOE_OK : cuda_fail(e, "linear launch");
+}
+template <int RG, bool GATED>
+k3moe_status linear_stream_t(const DeviceInfo &di, LinearStreamParams &a, cudaStream_t st) {
+    return a.p.T <= 8 ? launch_stream<RG, GATED, 1>(di, a, st) : launch_stream<RG, GATED, 2>(di, a, st);
 }
 
-// 8 weight rows per CTA while that makes up to about six CTAs per SM, else 16
-// (each CTA reads all of x).
-cudaError_t linear_stream(const DeviceInfo &di, const LinearParams &p, cudaStream_t st) {
-    const bool wide = ceil_div(p.N, 8) > 4 * di.sms;
-    if (p.wg) {
-        if (p.T <= 8) return wide ? launch_stream<2, true, 1>(di, p, st) : launch_stream<1, true, 1>(di, p, st);
-        return wide ? launch_stream<2, true, 2>(di, p, st) : launch_stream<1, true, 2>(di, p, st);
-    }
-    if (p.T <= 8) return wide ? launch_stream<2, false, 1>(di, p, st) : launch_stream<1, false, 1>(di, p, st);
-    return wide ? launch_stream<2, false, 2>(di, p, st) : launch_stream<1, false, 2>(di, p, st);
+// 8 output columns per CTA up to four CTAs per SM, else 16 (each CTA reads all
+// of x).
+k3moe_status linear_stream(const DeviceInfo &di, LinearStreamParams &a, cudaStream_t st) {
+    const bool wide = ceil_div(a.p.N, 8) > 4 * di.sms;
+    if (a.p.wg) return wide ? linear_stream_t<2, true>(di, a, st) : linear_stream_t<1, true>(di, a, st);
+    return wide ? linear_stream_t<2, false>(di, a, st) : linear_stream_t<1, false>(di, a, st);
 }
 
 k3moe_status linear_launch(const LinearParams &p, WsHeader *hdr, cudaStream_t st) {
     DeviceInfo *di;
     k3moe_status s = device_info(&di);
     if (s != K3MOE_OK) return s;
-    cudaError_t e;
     if (p.T <= kLsMaxT) {
-        e = linear_stream(*di, p, st);
-        return e == cudaSuccess ? K3MOE_OK : cuda_fail(e, "linear launch");
+        LinearStreamParams a;
+        a.p = p;
+        a.hdr = hdr;
+        a.wait_ns = wait_limit();
+        return linear_stream(*di, a, st);
     }
+    cudaError_t e;
     LinearTcParams a{};
     a.p = p;
     a.hdr = hdr;

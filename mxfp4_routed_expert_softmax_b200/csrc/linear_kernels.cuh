@@ -149,15 +149,30 @@ __device__ __forceinline__ void linear_bias(const float *bias, int n, int N, flo
 }
 
 // ------------------------------------------------------ few tokens: stream --
-// Up to 16 tokens: the weights are read once from memory and nothing else
-// counts, so they go straight from global memory into the operand registers
-// of warp-level MMAs (m16n8k16: A = 16 tokens, B = 8 weight rows), without
-// shared memory or a tensor-memory round trip.  A lane's 16-byte load holds 8
-// consecutive k of one weight row; the same k order is used for x, so the
-// order of k inside a 32-wide step is free and two MMAs take the 16 bytes as
-// they are.  Warps split K in 64-wide units (a whole 128-byte line of each
-// row), their sums are added in warp order.
+// Up to 16 tokens: the weights are read once from memory and little else
+// counts.  TMA brings a chunk of kc columns of the CTA's weight rows and of the
+// tokens into a ring of stages of each warp (chunk c belongs to warp c %
+// warps; zeros past the last row, token and column); the warp multiplies it
+// with warp-level MMAs (m16n8k16: A = 16 tokens, B = 8 weight rows), whose few
+// cycles do not show, so a tensor-memory round trip would only add to the
+// latency.  A lane's 16 bytes hold 8 consecutive k of one row; the same k
+// order is used for weights and tokens, so the order of k inside a step is
+// free and two MMAs take them as they are.  (Loads straight into the operand
+// registers, 8 lines each: one token's 896 x 7168 took 4.4 us to arrive; bulk
+// copies of 512-byte rows: 4.7 us.)
 constexpr int kLsMaxT = 16;
+constexpr int kLsWarps = 8;
+constexpr int kLsMaxStages = 4;
+
+struct LinearStreamParams {
+    alignas(64) uint4 tw[8];
+    alignas(64) uint4 twg[8];
+    alignas(64) uint4 tx[8];
+    LinearParams p;
+    int kc, ns;  // columns per chunk (a multiple of 64), stages per warp
+    WsHeader *hdr;
+    uint64_t wait_ns;
+};
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1) {
@@ -167,104 +182,138 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint4 ldg_once(const uint4 *p) {  // no reuse inside the kernel: past L1
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
+// NM groups of 8 weight rows (gated: all of w's, then w_gate's), TG 8-token halves.
+__host__ __device__ constexpr int ls_red_bytes(int nm, int tg) { return kLsWarps * nm * tg * 64 * 4; }
+__host__ __device__ constexpr int ls_stage_bytes(int nm, int tg, int kc) { return (nm + tg) * 8 * kc * 2; }
+__host__ __device__ constexpr int ls_smem_bytes(int nm, int tg, int kc, int ns) {
+    return 1024 + ls_red_bytes(nm, tg) + kLsWarps * ns * ls_stage_bytes(nm, tg, kc);
 }
 
-// RG: groups of 8 weight rows per CTA; TG: 8-token halves; U: 64-wide units
-// whose loads are in flight together.  Rows and tokens past the last are read
-// as the last one, and their sums dropped.
-template <int RG, bool GATED, int TG, int U>
-__global__ void __launch_bounds__(512, 1) linear_stream_kernel(const __grid_constant__ LinearParams p) {
-    constexpr int NM = RG * (GATED ? 2 : 1);
-    extern __shared__ float red[];  // [warps][NM][8 * TG tokens][8 rows]
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+// RG: groups of 8 output columns per CTA.
+template <int RG, bool GATED, int TG>
+__global__ void __launch_bounds__(32 * kLsWarps) linear_stream_kernel(const __grid_constant__ LinearStreamParams a) {
+    constexpr int NM = RG * (GATED ? 2 : 1), TT = 8 * TG;
+    extern __shared__ __align__(128) uint8_t ls_raw[];
+    uint64_t *bars = reinterpret_cast<uint64_t *>(ls_raw);  // [warp][stage]
+    volatile int *s_abort = reinterpret_cast<volatile int *>(ls_raw + 512);
+    float *red = reinterpret_cast<float *>(ls_raw + 1024);  // [warp][NM][TT tokens][8 rows]
+    const LinearParams &p = a.p;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, q = lane & 3;
     const int n0 = blockIdx.x * RG * 8;
-    const uint16_t *wr[NM], *xr[TG];
-#pragma unroll
-    for (int r = 0; r < NM; ++r)
-        wr[r] = (GATED && (r & 1) ? p.wg : p.w) + (long long)min(n0 + (GATED ? r >> 1 : r) * 8 + g, p.N - 1) * p.ldw + q * 8;
-#pragma unroll
-    for (int t = 0; t < TG; ++t) xr[t] = p.x + (long long)min(g + 8 * t, p.T - 1) * p.ldx + q * 8;
-    pdl_wait();
-    pdl_trigger();
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    float sum[NM][4] = {};
-    auto step = [&](float (&d)[4], const uint4 &xa, const uint4 &xb, const uint4 &w) {
-        mma_16816(d, xa.x, xb.x, xa.y, xb.y, w.x, w.y);
-        mma_16816(d, xa.z, xb.z, xa.w, xb.w, w.z, w.w);
-    };
-    const int units = ceil_div(p.K, 64);
-    for (int u = warp; u < units; u += nw * U) {
-        // units past the last are read as this warp's first and not used; in
-        // the last unit, k past K is read as the row's last 8 and replaced by 0
-        uint4 w[U][2][NM], x[U][2][TG];
-        auto at = [&](int i, int h) { return min((u + i * nw < units ? u + i * nw : u) * 64 + h * 32, p.K - 8 - q * 8); };
-#pragma unroll
-        for (int i = 0; i < U; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int r = 0; r < NM; ++r) w[i][h][r] = ldg_once(reinterpret_cast<const uint4 *>(wr[r] + at(i, h)));
-#pragma unroll
-        for (int i = 0; i < U; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int t = 0; t < TG; ++t) x[i][h][t] = __ldg(reinterpret_cast<const uint4 *>(xr[t] + at(i, h)));
-        float part[NM][4] = {};  // chains of 4 U steps; the rest is added in fp32
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int k = (u + i * nw) * 64;
-            if (u + i * nw >= units) break;
-            if (k + 64 > p.K) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (k + h * 32 + q * 8 >= p.K) {
-#pragma unroll
-                        for (int r = 0; r < NM; ++r) w[i][h][r] = zero;
-#pragma unroll
-                        for (int t = 0; t < TG; ++t) x[i][h][t] = zero;
-                    }
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int r = 0; r < NM; ++r) step(part[r], x[i][h][0], TG == 2 ? x[i][h][TG - 1] : zero, w[i][h][r]);
+    const int T = p.T, rowb = a.kc * 2, stageb = (NM + TG) * 8 * rowb;
+    uint8_t *ring = ls_raw + 1024 + ls_red_bytes(NM, TG) + warp * a.ns * stageb;
+    uint64_t *bar = bars + warp * kLsMaxStages;
+    if (lane == 0) {
+        for (int s = 0; s < a.ns; ++s) mbar_init(&bar[s], 1);
+        fence_mbar_init();
+        if (warp == 0) {
+            *s_abort = 0;
+            umma::prefetch_tmap(a.tw);
+            if (GATED) umma::prefetch_tmap(a.twg);
+            umma::prefetch_tmap(a.tx);
         }
-#pragma unroll
-        for (int r = 0; r < NM; ++r)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) sum[r][c] += part[r][c];
-    }
-    constexpr int TT = 8 * TG;
-#pragma unroll
-    for (int r = 0; r < NM; ++r) {
-        float *o = red + (warp * NM + r) * TT * 8 + g * 8 + 2 * q;  // token g, rows 2q and 2q + 1
-        *reinterpret_cast<float2 *>(o) = make_float2(sum[r][0], sum[r][1]);
-        if (TG == 2) *reinterpret_cast<float2 *>(o + 64) = make_float2(sum[r][2], sum[r][3]);
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < RG * TT * 8; i += blockDim.x) {
-        const int rg = i / (TT * 8), t = (i / 8) % TT, n = n0 + rg * 8 + i % 8;
-        if (t >= p.T || n >= p.N) continue;
-        float b[1], bg[1], v[1] = {0.f}, gv[1] = {0.f};
-        linear_bias(p.bias, n, p.N, b);
-        linear_bias(p.bias_g, n, p.N, bg);
-        Residual<1> res;
-        linear_resid(p, t, n, res, p.out_fp32);
-        const float *src = red + (GATED ? 2 * rg : rg) * TT * 8 + i % (TT * 8);
-#pragma unroll 4
-        for (int w = 0; w < nw; ++w) {
-            v[0] += src[w * NM * TT * 8];
-            if (GATED) gv[0] += src[(w * NM + 1) * TT * 8];
+    pdl_wait();
+    pdl_trigger();
+    const int chunks = ceil_div(p.K, a.kc);
+    auto issue = [&](int c, int s) {
+        if (umma::elect()) {
+            uint8_t *st = ring + s * stageb;
+            mbar_arrive_expect_tx(&bar[s], (uint32_t)stageb);
+            umma::tma_load_2d(st, a.tw, c * a.kc, n0, &bar[s]);
+            if (GATED) umma::tma_load_2d(st + RG * 8 * rowb, a.twg, c * a.kc, n0, &bar[s]);
+            umma::tma_load_2d(st + NM * 8 * rowb, a.tx, c * a.kc, 0, &bar[s]);
         }
-        linear_finish(p, t, n, v, gv, b, bg, res, GATED, p.resid != nullptr, p.out_fp32);
+        __syncwarp();
+    };
+    int issued = 0;
+    for (int s = 0; s < a.ns; ++s)
+        if (warp + s * kLsWarps < chunks) {
+            issue(warp + s * kLsWarps, s);
+            ++issued;
+        }
+    // this thread's output, and what goes into it beside the sums
+    const int ot = (threadIdx.x / 8) % TT, on = n0 + threadIdx.x / (TT * 8) * 8 + threadIdx.x % 8;
+    const bool out = threadIdx.x < RG * TT * 8 && ot < T && on < p.N;
+    float b[1], bg[1];
+    Residual<1> res;
+    if (out) {
+        linear_bias(p.bias, on, p.N, b);
+        linear_bias(p.bias_g, on, p.N, bg);
+        linear_resid(p, ot, on, res, p.out_fp32);
+    }
+    __syncwarp();
+    const bool odd = (g & 1) != 0;
+    // 64 columns of row r of a stage, columns 8 q.. of the first and of the
+    // second 32; odd rows read them in the other order (no bank conflicts)
+    auto row64 = [&](const uint8_t *row, uint4 (&v)[2]) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(row + (odd ? 64 : 0));
+        const uint4 y = *reinterpret_cast<const uint4 *>(row + (odd ? 0 : 64));
+        v[0] = odd ? y : x;
+        v[1] = odd ? x : y;
+    };
+    float sum[NM][4] = {};
+    int s = 0;
+    uint32_t ph = 0u;
+    for (int c = warp; c < chunks; c += kLsWarps) {
+        if (!mbar_wait_warp(&bar[s], ph, a.hdr, a.wait_ns, s_abort)) break;
+        const uint8_t *st = ring + s * stageb + g * rowb + q * 16;
+        float part[NM][4] = {};  // a chain per chunk; the chunks are added in fp32
+#pragma unroll 2
+        for (int k = 0; k < rowb; k += 128) {
+            uint4 x[TG][2];
+#pragma unroll
+            for (int t = 0; t < TG; ++t) row64(st + (NM + t) * 8 * rowb + k, x[t]);
+#pragma unroll
+            for (int m = 0; m < NM; ++m) {
+                uint4 w[2];
+                row64(st + m * 8 * rowb + k, w);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint4 &xa = x[0][h], &xb = x[TG - 1][h];
+                    mma_16816(part[m], xa.x, TG == 2 ? xb.x : 0u, xa.y, TG == 2 ? xb.y : 0u, w[h].x, w[h].y);
+                    mma_16816(part[m], xa.z, TG == 2 ? xb.z : 0u, xa.w, TG == 2 ? xb.w : 0u, w[h].z, w[h].w);
+                }
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[m][e] += part[m][e];
+        __syncwarp();
+        if (c + a.ns * kLsWarps < chunks) {
+            issue(c + a.ns * kLsWarps, s);
+            ++issued;
+        }
+        if (++s == a.ns) {
+            s = 0;
+            ph ^= 1u;
+        }
+    }
+    if (*s_abort && lane == 0) {
+        // a wait gave up: wait (bounded) for this warp's copies in flight
+        for (int i = 0; i < a.ns && i < issued; ++i) mbar_drain(&bar[i], (uint32_t)(((issued - 1 - i) / a.ns) & 1), a.wait_ns);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int m = 0; m < NM; ++m) {
+        float *o = red + (warp * NM + m) * TT * 8 + g * 8 + 2 * q;  // token g, rows 2q and 2q + 1
+        *reinterpret_cast<float2 *>(o) = make_float2(sum[m][0], sum[m][1]);
+        if (TG == 2) *reinterpret_cast<float2 *>(o + 64) = make_float2(sum[m][2], sum[m][3]);
+    }
+    __syncthreads();
+    if (out) {
+        float v[1] = {0.f}, gv[1] = {0.f};
+        const int rg = threadIdx.x / (TT * 8);
+        const float *src = red + rg * TT * 8 + threadIdx.x % (TT * 8);
+#pragma unroll
+        for (int w = 0; w < kLsWarps; ++w) {
+            v[0] += src[w * NM * TT * 8];
+            if (GATED) gv[0] += src[(w * NM + RG) * TT * 8];
+        }
+        linear_finish(p, ot, on, v, gv, b, bg, res, GATED, p.resid != nullptr, p.out_fp32);
     }
 }
 
@@ -299,8 +348,6 @@ struct LinearTcParams {
     WsHeader *hdr;
     uint64_t wait_ns;
 };
-
-__device__ __forceinline__ void prefetch_tmap(const void *m) { asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory"); }
 
 // A tile of 128 weight rows x bn tokens per cluster of `split` CTAs, which
 // share its K: each accumulates its part, sends every CTA of the cluster the
@@ -345,8 +392,8 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
         *s_abort = 0;
     }
     if (warp == kLtEpi && lane == 0) {
-        prefetch_tmap(a.tw);
-        prefetch_tmap(a.tx);
+        umma::prefetch_tmap(a.tw);
+        umma::prefetch_tmap(a.tx);
     }
     if (warp == 0) umma::tmem_alloc(tslot, (uint32_t)a.tcols);
     umma::fence_before();
@@ -564,8 +611,8 @@ __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid
         *s_abort = 0;
     }
     if (warp == kLpEpi && lane == 0) {
-        prefetch_tmap(a.tw);
-        prefetch_tmap(a.tx);
+        umma::prefetch_tmap(a.tw);
+        umma::prefetch_tmap(a.tx);
     }
     if (warp == 0) umma::tmem_alloc_pair(tslot, 512u);
     umma::fence_before();

@@ -148,6 +148,10 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const void *tmap, int x, 
         : "memory");
 }
 
+__device__ __forceinline__ void prefetch_tmap(const void *tmap) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory");
+}
+
 // Point a tensor map held in global memory at another global address (the
 // rest of the map is unchanged), then publish it to the tensormap proxy.
 __device__ __forceinline__ void tmap_set_address(void *gmap, const void *addr) {
