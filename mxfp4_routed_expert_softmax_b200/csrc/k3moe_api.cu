@@ -894,26 +894,30 @@ cudaError_t launch_cluster(Kern kernel, int grid, int block, size_t smem, int n,
 }
 
 // -------------------------------------------------------- dense product --
-// Chunks of up to 256 columns, at least one per warp where K allows, and as
-// many stages as the CTAs that share an SM have room for (all of K in flight
-// up to there).
+// Chunks of up to 256 columns, at least one per warp where K allows, and up to
+// four stages per warp, all of K where they hold it.  Up to 8 tokens: two CTAs
+// per SM at most, which go from group to group of columns (one streams while
+// the other starts or ends a group): 8 x 7168 x 7168 in 19 us, 27 with a CTA
+// per group.  More tokens: their stages are too large for that (16 x 7168 x
+// 7168: 48 us, against 27 with a CTA per group, as many per SM as fit).
 template <int RG, bool GATED, int TG>
 k3moe_status launch_stream(const DeviceInfo &di, LinearStreamParams &a, cudaStream_t st) {
     constexpr int NM = RG * (GATED ? 2 : 1);
     const LinearParams &p = a.p;
-    const int ctas = ceil_div(p.N, 8 * RG);
-    const int per_sm = std::min(ceil_div(ctas, di.sms), 4);
+    const int groups = ceil_div(p.N, 8 * RG);
+    const int per_sm = std::min(ceil_div(groups, di.sms), TG == 1 ? 2 : 4);
+    const int ctas = TG == 1 ? std::min(groups, per_sm * di.sms) : groups;
     for (a.kc = std::min(256, ceil_div(ceil_div(p.K, kLsWarps), 64) * 64);; a.kc -= 64) {
-        const int rounds = ceil_div(ceil_div(p.K, a.kc), kLsWarps);
+        const int rounds = ceil_div(ceil_div(p.K, a.kc), kLsWarps) * ceil_div(groups, ctas);
         auto fits = [&](int ns, int n) { return n * (ls_smem_bytes(NM, TG, a.kc, ns) + 1024) <= kSmemLimit + 1024; };
         a.ns = std::min(rounds, kLsMaxStages);
         while (a.ns > 1 && !fits(a.ns, per_sm)) --a.ns;
-        if (a.ns == 1 && rounds > 1 && fits(2, 1)) a.ns = 2;  // one CTA fewer per SM, but never a single stage
+        if (TG == 2 && a.ns == 1 && rounds > 1 && fits(2, 1)) a.ns = 2;  // fewer CTAs per SM, but never a single stage
         if (a.kc == 64 || (fits(a.ns, 1) && a.ns >= std::min(rounds, 2))) break;
     }
     k3moe_status s = tmap_bf16_rows(p.w, p.K, p.N, a.tw, p.ldw, 8 * RG, a.kc);
     if (s == K3MOE_OK && GATED) s = tmap_bf16_rows(p.wg, p.K, p.N, a.twg, p.ldw, 8 * RG, a.kc);
-    if (s == K3MOE_OK) s = tmap_bf16_rows(p.x, p.K, p.T, a.tx, p.ldx, 8 * TG, a.kc);
+    if (s == K3MOE_OK) s = tmap_bf16_rows(p.x, p.K, p.T, a.tx, p.ldx, p.T, a.kc);
     if (s != K3MOE_OK) return s;
     cudaError_t e =
         launch(linear_stream_kernel<RG, GATED, TG>, dim3(ctas), dim3(32 * kLsWarps),

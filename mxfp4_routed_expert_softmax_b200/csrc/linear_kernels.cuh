@@ -152,7 +152,7 @@ __device__ __forceinline__ void linear_bias(const float *bias, int n, int N, flo
 // Up to 16 tokens: the weights are read once from memory and little else
 // counts.  TMA brings a chunk of kc columns of the CTA's weight rows and of the
 // tokens into a ring of stages of each warp (chunk c belongs to warp c %
-// warps; zeros past the last row, token and column); the warp multiplies it
+// warps; zeros past the last row and column); the warp multiplies it
 // with warp-level MMAs (m16n8k16: A = 16 tokens, B = 8 weight rows), whose few
 // cycles do not show, so a tensor-memory round trip would only add to the
 // latency.  A lane's 16 bytes hold 8 consecutive k of one row; the same k
@@ -186,7 +186,7 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
 __host__ __device__ constexpr int ls_red_bytes(int nm, int tg) { return kLsWarps * nm * tg * 64 * 4; }
 __host__ __device__ constexpr int ls_stage_bytes(int nm, int tg, int kc) { return (nm + tg) * 8 * kc * 2; }
 __host__ __device__ constexpr int ls_smem_bytes(int nm, int tg, int kc, int ns) {
-    return 1024 + ls_red_bytes(nm, tg) + kLsWarps * ns * ls_stage_bytes(nm, tg, kc);
+    return 1024 + 2 * ls_red_bytes(nm, tg) + kLsWarps * ns * ls_stage_bytes(nm, tg, kc);
 }
 
 // RG: groups of 8 output columns per CTA.
@@ -196,13 +196,12 @@ __global__ void __launch_bounds__(32 * kLsWarps) linear_stream_kernel(const __gr
     extern __shared__ __align__(128) uint8_t ls_raw[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(ls_raw);  // [warp][stage]
     volatile int *s_abort = reinterpret_cast<volatile int *>(ls_raw + 512);
-    float *red = reinterpret_cast<float *>(ls_raw + 1024);  // [warp][NM][TT tokens][8 rows]
+    float *red = reinterpret_cast<float *>(ls_raw + 1024);  // [2][warp][NM][TT tokens][8 rows]
     const LinearParams &p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, q = lane & 3;
-    const int n0 = blockIdx.x * RG * 8;
     const int T = p.T, rowb = a.kc * 2, stageb = (NM + TG) * 8 * rowb;
-    uint8_t *ring = ls_raw + 1024 + ls_red_bytes(NM, TG) + warp * a.ns * stageb;
+    uint8_t *ring = ls_raw + 1024 + 2 * ls_red_bytes(NM, TG) + warp * a.ns * stageb;
     uint64_t *bar = bars + warp * kLsMaxStages;
     if (lane == 0) {
         for (int s = 0; s < a.ns; ++s) mbar_init(&bar[s], 1);
@@ -217,34 +216,27 @@ __global__ void __launch_bounds__(32 * kLsWarps) linear_stream_kernel(const __gr
     __syncthreads();
     pdl_wait();
     pdl_trigger();
-    const int chunks = ceil_div(p.K, a.kc);
-    auto issue = [&](int c, int s) {
+    const int chunks = ceil_div(p.K, a.kc), groups = ceil_div(p.N, RG * 8);
+    // The warp's next chunk to copy: it runs on into the CTA's next groups of
+    // columns while the sums of one are brought together.
+    int ig = warp < chunks ? blockIdx.x : groups, ic = warp, issued = 0;
+    auto issue = [&](int s) {
+        if (ig >= groups) return;
         if (umma::elect()) {
             uint8_t *st = ring + s * stageb;
-            mbar_arrive_expect_tx(&bar[s], (uint32_t)stageb);
-            umma::tma_load_2d(st, a.tw, c * a.kc, n0, &bar[s]);
-            if (GATED) umma::tma_load_2d(st + RG * 8 * rowb, a.twg, c * a.kc, n0, &bar[s]);
-            umma::tma_load_2d(st + NM * 8 * rowb, a.tx, c * a.kc, 0, &bar[s]);
+            mbar_arrive_expect_tx(&bar[s], (uint32_t)((NM * 8 + T) * rowb));  // the other token rows stay as they are
+            umma::tma_load_2d(st, a.tw, ic * a.kc, ig * RG * 8, &bar[s]);
+            if (GATED) umma::tma_load_2d(st + RG * 8 * rowb, a.twg, ic * a.kc, ig * RG * 8, &bar[s]);
+            umma::tma_load_2d(st + NM * 8 * rowb, a.tx, ic * a.kc, 0, &bar[s]);
         }
         __syncwarp();
-    };
-    int issued = 0;
-    for (int s = 0; s < a.ns; ++s)
-        if (warp + s * kLsWarps < chunks) {
-            issue(warp + s * kLsWarps, s);
-            ++issued;
+        ++issued;
+        if ((ic += kLsWarps) >= chunks) {
+            ic = warp;
+            ig += gridDim.x;
         }
-    // this thread's output, and what goes into it beside the sums
-    const int ot = (threadIdx.x / 8) % TT, on = n0 + threadIdx.x / (TT * 8) * 8 + threadIdx.x % 8;
-    const bool out = threadIdx.x < RG * TT * 8 && ot < T && on < p.N;
-    float b[1], bg[1];
-    Residual<1> res;
-    if (out) {
-        linear_bias(p.bias, on, p.N, b);
-        linear_bias(p.bias_g, on, p.N, bg);
-        linear_resid(p, ot, on, res, p.out_fp32);
-    }
-    __syncwarp();
+    };
+    for (int s = 0; s < a.ns; ++s) issue(s);
     const bool odd = (g & 1) != 0;
     // 64 columns of row r of a stage, columns 8 q.. of the first and of the
     // second 32; odd rows read them in the other order (no bank conflicts)
@@ -254,66 +246,79 @@ __global__ void __launch_bounds__(32 * kLsWarps) linear_stream_kernel(const __gr
         v[0] = odd ? y : x;
         v[1] = odd ? x : y;
     };
-    float sum[NM][4] = {};
-    int s = 0;
+    const int rg = threadIdx.x / (TT * 8), ot = (threadIdx.x / 8) % TT;  // this thread's output of a group
+    int s = 0, par = 0;
     uint32_t ph = 0u;
-    for (int c = warp; c < chunks; c += kLsWarps) {
-        if (!mbar_wait_warp(&bar[s], ph, a.hdr, a.wait_ns, s_abort)) break;
-        const uint8_t *st = ring + s * stageb + g * rowb + q * 16;
-        float part[NM][4] = {};  // a chain per chunk; the chunks are added in fp32
+    bool ok = true;
+    for (int grp = blockIdx.x; grp < groups; grp += gridDim.x, par ^= 1) {
+        const int on = grp * RG * 8 + rg * 8 + threadIdx.x % 8;
+        const bool out = rg < RG && ot < T && on < p.N;
+        float b[1], bg[1];
+        Residual<1> res;
+        if (out) {
+            linear_bias(p.bias, on, p.N, b);
+            linear_bias(p.bias_g, on, p.N, bg);
+            linear_resid(p, ot, on, res, p.out_fp32);
+        }
+        __syncwarp();
+        float sum[NM][4] = {};
+        for (int c = warp; c < chunks; c += kLsWarps) {
+            ok = ok && mbar_wait_warp(&bar[s], ph, a.hdr, a.wait_ns, s_abort);
+            if (!ok) break;
+            const uint8_t *st = ring + s * stageb + g * rowb + q * 16;
+            float part[NM][4] = {};  // a chain per chunk; the chunks are added in fp32
 #pragma unroll 2
-        for (int k = 0; k < rowb; k += 128) {
-            uint4 x[TG][2];
+            for (int k = 0; k < rowb; k += 128) {
+                uint4 x[TG][2];
 #pragma unroll
-            for (int t = 0; t < TG; ++t) row64(st + (NM + t) * 8 * rowb + k, x[t]);
+                for (int t = 0; t < TG; ++t) row64(st + (NM + t) * 8 * rowb + k, x[t]);
 #pragma unroll
-            for (int m = 0; m < NM; ++m) {
-                uint4 w[2];
-                row64(st + m * 8 * rowb + k, w);
+                for (int m = 0; m < NM; ++m) {
+                    uint4 w[2];
+                    row64(st + m * 8 * rowb + k, w);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint4 &xa = x[0][h], &xb = x[TG - 1][h];
-                    mma_16816(part[m], xa.x, TG == 2 ? xb.x : 0u, xa.y, TG == 2 ? xb.y : 0u, w[h].x, w[h].y);
-                    mma_16816(part[m], xa.z, TG == 2 ? xb.z : 0u, xa.w, TG == 2 ? xb.w : 0u, w[h].z, w[h].w);
+                    for (int h = 0; h < 2; ++h) {
+                        const uint4 &xa = x[0][h], &xb = x[TG - 1][h];
+                        mma_16816(part[m], xa.x, TG == 2 ? xb.x : 0u, xa.y, TG == 2 ? xb.y : 0u, w[h].x, w[h].y);
+                        mma_16816(part[m], xa.z, TG == 2 ? xb.z : 0u, xa.w, TG == 2 ? xb.w : 0u, w[h].z, w[h].w);
+                    }
                 }
             }
+#pragma unroll
+            for (int m = 0; m < NM; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum[m][e] += part[m][e];
+            __syncwarp();
+            issue(s);
+            if (++s == a.ns) {
+                s = 0;
+                ph ^= 1u;
+            }
         }
-#pragma unroll
-        for (int m = 0; m < NM; ++m)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sum[m][e] += part[m][e];
         __syncwarp();
-        if (c + a.ns * kLsWarps < chunks) {
-            issue(c + a.ns * kLsWarps, s);
-            ++issued;
+        float *rbuf = red + par * (ls_red_bytes(NM, TG) / 4);
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+            float *o = rbuf + (warp * NM + m) * TT * 8 + g * 8 + 2 * q;  // token g, rows 2q and 2q + 1
+            *reinterpret_cast<float2 *>(o) = make_float2(sum[m][0], sum[m][1]);
+            if (TG == 2) *reinterpret_cast<float2 *>(o + 64) = make_float2(sum[m][2], sum[m][3]);
         }
-        if (++s == a.ns) {
-            s = 0;
-            ph ^= 1u;
+        __syncthreads();
+        if (out) {
+            float v[1] = {0.f}, gv[1] = {0.f};
+            const float *src = rbuf + rg * TT * 8 + threadIdx.x % (TT * 8);
+#pragma unroll
+            for (int w = 0; w < kLsWarps; ++w) {
+                v[0] += src[w * NM * TT * 8];
+                if (GATED) gv[0] += src[(w * NM + RG) * TT * 8];
+            }
+            linear_finish(p, ot, on, v, gv, b, bg, res, GATED, p.resid != nullptr, p.out_fp32);
         }
+        __syncwarp();
     }
     if (*s_abort && lane == 0) {
         // a wait gave up: wait (bounded) for this warp's copies in flight
         for (int i = 0; i < a.ns && i < issued; ++i) mbar_drain(&bar[i], (uint32_t)(((issued - 1 - i) / a.ns) & 1), a.wait_ns);
-    }
-    __syncwarp();
-#pragma unroll
-    for (int m = 0; m < NM; ++m) {
-        float *o = red + (warp * NM + m) * TT * 8 + g * 8 + 2 * q;  // token g, rows 2q and 2q + 1
-        *reinterpret_cast<float2 *>(o) = make_float2(sum[m][0], sum[m][1]);
-        if (TG == 2) *reinterpret_cast<float2 *>(o + 64) = make_float2(sum[m][2], sum[m][3]);
-    }
-    __syncthreads();
-    if (out) {
-        float v[1] = {0.f}, gv[1] = {0.f};
-        const int rg = threadIdx.x / (TT * 8);
-        const float *src = red + rg * TT * 8 + threadIdx.x % (TT * 8);
-#pragma unroll
-        for (int w = 0; w < kLsWarps; ++w) {
-            v[0] += src[w * NM * TT * 8];
-            if (GATED) gv[0] += src[(w * NM + RG) * TT * 8];
-        }
-        linear_finish(p, ot, on, v, gv, b, bg, res, GATED, p.resid != nullptr, p.out_fp32);
     }
 }
 
