@@ -130,10 +130,12 @@ __device__ __noinline__ void gate_exact(const GateParams &p, long long t, GateEx
 // One warp per token, its logits in registers (lane l holds ids 128 i + 4 l ..
 // + 3).  The selection is a filter with an error bound:
 //   - without a bias the ranking is the logits' own and exact; with one the
-//     values c_e are formed in 32 bits, each within eps of the true one;
+//     values c_e are formed in 32 bits, each within eps of the true one
+//     (sigmoid scores first by the hardware's tanh, within 2^-10);
 //   - the k-th largest of the 32 lanes' maxima is a value that at least k
 //     values reach, so only those no more than 2 eps below it can be among the
-//     k largest (about 22 of 896 for k = 16): they go to shared memory;
+//     k largest (about 22 of 896 for k = 16): they go to a list, where sigmoid
+//     scores are formed again more exactly;
 //   - each candidate's place is the number of larger ones (ties to the lower
 //     id); where two neighbours of the list are within 2 eps, the candidates'
 //     values are formed again in 64 bits and placed by those.
@@ -142,19 +144,25 @@ __device__ __noinline__ void gate_exact(const GateParams &p, long long t, GateEx
 // gate_exact, so the result is that of the 64-bit definition in every case.
 // Weights are 32-bit: the scores of the picks from expf, the softmax's argument
 // l - max with its rounding error carried along.
+//
+// Bound by instruction issue (896 experts: about 20 per logit, for 4 bytes);
+// 4096 tokens x 896, softmax, top 16: 1450 instructions a token with a
+// compare-and-store per logit and 8.0 us, and what it takes now in the design
+// notes' table.
 constexpr int kGateWarps = 4;
-constexpr int kGateCap = 256;
+constexpr int kGateCap = 160;
 struct alignas(16) GateWarp {
     uint64_t key[kGateCap];   // value (order-preserving bits) above the inverted id
     double exact[kGateCap];
-    float top[32];
+    uint32_t top[32];
     float sorted[kGateMaxK + 1];
     int32_t id[kGateMaxK + 1];
 };
-static_assert(sizeof(GateExact) % 16 == 0 && sizeof(GateWarp) % 16 == 0, "16-byte parts of shared memory");
+static_assert(sizeof(GateWarp) % 16 == 0, "16-byte parts of shared memory");
 
-__host__ __device__ inline int gate_smem(int E, int groups) {
-    return (int)sizeof(GateExact) + kGateWarps * ((int)sizeof(GateWarp) + (groups > 1 ? E * 4 : 0));
+__host__ __device__ inline int gate_smem(int ni) {
+    const int warps = kGateWarps * ((int)sizeof(GateWarp) + ni * 512);
+    return warps > (int)sizeof(GateExact) ? warps : (int)sizeof(GateExact);
 }
 
 __device__ __forceinline__ uint32_t order_bits(float v) {
@@ -164,15 +172,30 @@ __device__ __forceinline__ uint32_t order_bits(float v) {
 __device__ __forceinline__ float from_order_bits(uint32_t b) {
     return __uint_as_float(b & 0x80000000u ? b ^ 0x80000000u : ~b);
 }
+__device__ __forceinline__ float ex2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float tanh_approx(float x) {
+    float y;
+    asm("tanh.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 template <int NI, bool BIAS>
 __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_constant__ GateParams p) {
     extern __shared__ __align__(16) uint8_t gate_raw[];
     constexpr int N = 4 * NI;
+    constexpr float kLog2e = 1.44269504088896341f;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    GateExact &slow = *reinterpret_cast<GateExact *>(gate_raw);
-    GateWarp &s = reinterpret_cast<GateWarp *>(gate_raw + sizeof(GateExact))[warp];
-    float *gbuf = reinterpret_cast<float *>(gate_raw + sizeof(GateExact) + kGateWarps * sizeof(GateWarp)) + warp * p.E;
+    GateWarp &s = *reinterpret_cast<GateWarp *>(gate_raw + warp * (sizeof(GateWarp) + NI * 512));
+    float *val = reinterpret_cast<float *>(&s + 1);  // [128 NI] what the experts are ranked by
     const long long t = (long long)blockIdx.x * kGateWarps + warp;
     const float ninf = -INFINITY;
     const uint32_t all = 0xffffffffu;
@@ -180,102 +203,109 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
     pdl_trigger();
     bool unsettled = false;
     if (t < p.T) {
-        float l[N], o[N];
+        float o[N], b[BIAS ? N : 1];  // o: the logits, then what the experts are ranked by
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             const int e = 128 * i + 4 * lane;
             if (p.vec && e + 4 <= p.E) {
                 if (p.bf16) {
                     const uint2 v = *reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(p.logits) + t * p.ld + e);
-                    l[4 * i] = bf16_lo(v.x), l[4 * i + 1] = bf16_hi(v.x), l[4 * i + 2] = bf16_lo(v.y), l[4 * i + 3] = bf16_hi(v.y);
+                    o[4 * i] = bf16_lo(v.x), o[4 * i + 1] = bf16_hi(v.x), o[4 * i + 2] = bf16_lo(v.y), o[4 * i + 3] = bf16_hi(v.y);
                 } else {
                     const float4 v = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p.logits) + t * p.ld + e);
-                    l[4 * i] = v.x, l[4 * i + 1] = v.y, l[4 * i + 2] = v.z, l[4 * i + 3] = v.w;
+                    o[4 * i] = v.x, o[4 * i + 1] = v.y, o[4 * i + 2] = v.z, o[4 * i + 3] = v.w;
                 }
             } else {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) l[4 * i + c] = e + c < p.E ? gate_logit(p, t, e + c) : ninf;
+                for (int c = 0; c < 4; ++c) o[4 * i + c] = e + c < p.E ? gate_logit(p, t, e + c) : ninf;
             }
-            if (BIAS) {
+            if constexpr (BIAS) {
                 if (p.vec && e + 4 <= p.E) {
                     const float4 v = *reinterpret_cast<const float4 *>(p.bias + e);
-                    o[4 * i] = v.x, o[4 * i + 1] = v.y, o[4 * i + 2] = v.z, o[4 * i + 3] = v.w;
+                    b[4 * i] = v.x, b[4 * i + 1] = v.y, b[4 * i + 2] = v.z, b[4 * i + 3] = v.w;
                 } else {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) o[4 * i + c] = e + c < p.E ? p.bias[e + c] : 0.f;
+                    for (int c = 0; c < 4; ++c) b[4 * i + c] = e + c < p.E ? p.bias[e + c] : 0.f;
                 }
             }
         }
-        float mx = ninf;
+        float lm = ninf, mx = ninf, sum = 0.f, inv = 0.f;  // lm: the lane's largest
+        if (!BIAS || !p.sigmoid) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) mx = fmaxf(mx, l[i]);  // passes over NaN
-        for (int q = 16; q > 0; q >>= 1) mx = fmaxf(mx, __shfl_xor_sync(all, mx, q));
-        float sum = 0.f, inv = 0.f;
+            for (int i = 0; i < N; ++i) lm = fmaxf(lm, o[i]);  // passes over NaN
+        }
         if (!p.sigmoid) {
-            // NaN and +inf logits make it NaN, as the formula does; __expf's
-            // error (2 units and |x| half units) is small where the term is
+            mx = lm;
+            for (int q = 16; q > 0; q >>= 1) mx = fmaxf(mx, __shfl_xor_sync(all, mx, q));
+            // NaN and +inf logits make the sum NaN, as the formula does; the
+            // exponential's error (2 units and |x| half units) is small where
+            // the term is
             if (mx > ninf) {
                 float part[4] = {};
 #pragma unroll
-                for (int i = 0; i < N; ++i) part[i % 4] += __expf(l[i] - mx);
+                for (int i = 0; i < N; ++i) part[i % 4] += ex2_approx((o[i] - mx) * kLog2e);
                 sum = (part[0] + part[1]) + (part[2] + part[3]);
                 for (int q = 16; q > 0; q >>= 1) sum += __shfl_xor_sync(all, sum, q);
                 inv = 1.0f / sum;  // the largest score
             }
         }
         // A score in 32 bits: within 2^-20 (sigmoid) or 2^-18 of the largest (softmax).
-        auto rough = [&](float v) { return p.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-v)) : __expf(v - mx) * inv; };
-        const float rough_eps = p.sigmoid ? 0x1p-20f : inv * 0x1p-18f;
-        float eps = 0.f, amax = 0.f;
+        auto rough = [&](float v) {
+            return p.sigmoid ? rcp_approx(1.0f + ex2_approx(-v * kLog2e)) : ex2_approx((v - mx) * kLog2e) * inv;
+        };
+        const float fine = p.sigmoid ? 0x1p-20f : inv * 0x1p-18f;
+        const bool scores = !BIAS && p.groups > 1 && p.group_top > 1;  // groups are compared by scores
+        const bool coarse = BIAS && p.sigmoid && p.groups == 1;
+        if constexpr (BIAS) {
+            if (coarse) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            if (BIAS) {
-                const float c = rough(l[i]) + o[i];
-                o[i] = l[i] > ninf && c > ninf ? c + 0.f : ninf;
-                if (o[i] > ninf) amax = fmaxf(amax, fabsf(o[i]));
+                for (int i = 0; i < N; ++i) {
+                    const float c = fmaf(0.5f, tanh_approx(0.5f * o[i]), 0.5f + b[i]);
+                    o[i] = o[i] > ninf ? fmaxf(c, ninf) : ninf;  // NaN: out
+                }
             } else {
-                o[i] = l[i] > ninf ? l[i] + 0.f : ninf;  // -0 ranks as 0
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const float c = rough(o[i]) + b[i];
+                    o[i] = o[i] > ninf ? fmaxf(c, ninf) : ninf;
+                }
             }
-        }
-        if (BIAS) {
-            for (int q = 16; q > 0; q >>= 1) amax = fmaxf(amax, __shfl_xor_sync(all, amax, q));
-            eps = rough_eps + 0x1p-23f * amax;
-            if (!(eps < 0x1p100f)) {
-                unsettled = amax > 0.f;  // infinite biases; without one: NaN scores, no expert left
-                eps = 0.f;
-            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) o[i] = fmaxf(o[i], ninf);  // NaN: out
         }
         if (p.groups > 1) {
-            // lanes-per-group lanes scan a group for its one or two largest values
+            // lp lanes scan a group for its one or two largest values
             const int gs = p.E / p.groups;
-            const bool scores = !BIAS && p.group_top > 1;
+            float amax = 0.f;
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int e = 128 * (i / 4) + 4 * lane + i % 4;
-                float v = o[i];
-                if (scores && v > ninf) {
-                    v = rough(l[i]);
-                    if (!(v > ninf)) v = ninf;
+            for (int i = 0; i < NI; ++i) {
+                float v[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    v[c] = o[4 * i + c];
+                    if (scores && v[c] > ninf) v[c] = fmaxf(rough(v[c]), ninf);
+                    if (v[c] > ninf) amax = fmaxf(amax, fabsf(v[c]));
                 }
-                if (e < p.E) gbuf[e] = v;
+                *reinterpret_cast<float4 *>(val + 128 * i + 4 * lane) = make_float4(v[0], v[1], v[2], v[3]);
             }
             __syncwarp();
             int lp = 32;
             while (lp * p.groups > 32) lp >>= 1;
             const int g = lane / lp;
-            float a = ninf, b = ninf;
+            float x1 = ninf, x2 = ninf;
             if (g < p.groups)
                 for (int e = lane % lp; e < gs; e += lp) {
-                    const float v = gbuf[g * gs + e];
-                    b = fmaxf(b, fminf(a, v));
-                    a = fmaxf(a, v);
+                    const float v = val[g * gs + e];
+                    x2 = fmaxf(x2, fminf(x1, v));
+                    x1 = fmaxf(x1, v);
                 }
             for (int q = 1; q < lp; q <<= 1) {
-                const float a2 = __shfl_xor_sync(all, a, q), b2 = __shfl_xor_sync(all, b, q);
-                b = fmaxf(fmaxf(b, b2), fminf(a, a2));
-                a = fmaxf(a, a2);
+                const float y1 = __shfl_xor_sync(all, x1, q), y2 = __shfl_xor_sync(all, x2, q);
+                x2 = fmaxf(fmaxf(x2, y2), fminf(x1, y1));
+                x1 = fmaxf(x1, y1);
             }
-            float v = p.group_top > 1 ? (b > ninf ? a + b : ninf) : a;
+            float v = p.group_top > 1 ? (x2 > ninf ? x1 + x2 : ninf) : x1;
             v = __shfl_sync(all, v, (lane * lp) & 31);
             int r = 0;
             for (int h = 0; h < p.groups; ++h) {
@@ -286,10 +316,12 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
             const uint32_t keep = __ballot_sync(all, is && r < p.kept);
             if (BIAS || scores) {
                 // the last group kept and the first one dropped must differ by more than their errors
+                for (int q = 16; q > 0; q >>= 1) amax = fmaxf(amax, __shfl_xor_sync(all, amax, q));
                 const float vk = __shfl_sync(all, v, __ffs(__ballot_sync(all, is && r == p.kept - 1)) - 1);
                 const float vd = __shfl_sync(all, v, __ffs(__ballot_sync(all, is && r == p.kept)) - 1);
-                const float geps = p.group_top * (BIAS ? eps : rough_eps) + 0x1p-23f * fmaxf(fabsf(vk), fabsf(vd));
+                const float geps = p.group_top * (fine + 0x1p-22f * amax);
                 if (vk > ninf && vd > ninf && !(vk - vd > 2.f * geps)) unsettled = true;
+                if (amax == INFINITY) unsettled = true;
             }
             const uint32_t m = (0x100000u + gs - 1) / gs;  // e / gs = e m >> 20 for e < 1024
 #pragma unroll
@@ -298,24 +330,43 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
                 if (!((keep >> ((e * m) >> 20 & 31)) & 1u)) o[i] = ninf;
             }
         }
-        // the k-th largest lane maximum
-        float lm = ninf;
+        if (BIAS || p.groups > 1) {
+            lm = ninf;
 #pragma unroll
-        for (int i = 0; i < N; ++i) lm = fmaxf(lm, o[i]);
-        s.top[lane] = lm;
+            for (int i = 0; i < N; ++i) lm = fmaxf(lm, o[i]);
+            __syncwarp();
+        }
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+            *reinterpret_cast<float4 *>(val + 128 * i + 4 * lane) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        // The k-th largest lane maximum, from below: the keys leave out the
+        // last 5 bits, which tell the lanes apart.
+        const uint32_t mine_key = (order_bits(lm) & ~31u) | (31u - lane);
+        s.top[lane] = mine_key;
         __syncwarp();
         int r = 0;
 #pragma unroll
         for (int j = 0; j < 32; j += 4) {
-            const float4 v = *reinterpret_cast<const float4 *>(&s.top[j]);
-            r += (v.x > lm || (v.x == lm && j < lane)) + (v.y > lm || (v.y == lm && j + 1 < lane)) +
-                 (v.z > lm || (v.z == lm && j + 2 < lane)) + (v.w > lm || (v.w == lm && j + 3 < lane));
+            const uint4 v = *reinterpret_cast<const uint4 *>(&s.top[j]);
+            r += (v.x > mine_key) + (v.y > mine_key) + (v.z > mine_key) + (v.w > mine_key);
         }
-        const float th = __shfl_sync(all, lm, __ffs(__ballot_sync(all, r == p.k - 1)) - 1) - 2.f * eps;
-        // candidates
-        int cnt = 0;
+        const int at = __ffs(__ballot_sync(all, r == p.k - 1)) - 1;
+        const float low = __shfl_sync(all, lm, at);
+        const float top = __shfl_sync(all, lm, __ffs(__ballot_sync(all, r == 0)) - 1);
+        float th = low > ninf ? from_order_bits(order_bits(low) & ~31u) : ninf;
+        float eps = 0.f;
+        if (BIAS && top > ninf) {
+            // values of larger size than both are far below the threshold
+            const float size = 0x1p-22f * fmaxf(fabsf(top), low > ninf ? fabsf(low) : 0.f);
+            eps = fine + size;
+            th -= 2.f * ((coarse ? 0x1p-10f : fine) + size);
+            if (!(eps < 0x1p100f)) unsettled = true;  // infinite biases
+        }
+        th = fmaxf(th, -3.402823466e38f);  // -inf is out
+        uint32_t mask = 0u;
 #pragma unroll
-        for (int i = 0; i < N; ++i) cnt += o[i] > ninf && o[i] >= th ? 1 : 0;
+        for (int i = 0; i < N; ++i) mask |= o[i] >= th ? 1u << i : 0u;
+        const int cnt = __popc(mask);
         int pos = cnt;
 #pragma unroll
         for (int q = 1; q < 32; q <<= 1) {
@@ -326,14 +377,23 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
         pos -= cnt;
         if (C > kGateCap) unsettled = true;
         if (!unsettled) {  // alike in all lanes
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                if (o[i] > ninf && o[i] >= th)
-                    s.key[pos++] = (uint64_t)order_bits(o[i]) << 32 | (uint32_t)~(128 * (i / 4) + 4 * lane + i % 4);
+            int32_t *list = reinterpret_cast<int32_t *>(s.exact);
+            while (mask) {
+                const int i = __ffs(mask) - 1;
+                mask &= mask - 1u;
+                list[pos++] = 128 * (i >> 2) + 4 * lane + (i & 3);
+            }
+            __syncwarp();
+            for (int c = lane; c < C; c += 32) {
+                const int e = list[c];
+                const float v = coarse ? rough(gate_logit(p, t, e)) + p.bias[e] : val[e];
+                s.key[c] = (uint64_t)order_bits(v + 0.f) << 32 | (uint32_t)~e;  // -0 ranks as 0
+            }
             __syncwarp();
             for (int c = lane; c < C; c += 32) {
                 const uint64_t key = s.key[c];
                 int place = 0;
+#pragma unroll 4
                 for (int j = 0; j < C; ++j) place += s.key[j] > key ? 1 : 0;
                 if (place <= p.k) {
                     s.sorted[place] = from_order_bits((uint32_t)(key >> 32));
@@ -343,7 +403,8 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
             __syncwarp();
             const int got = min(C, p.k);
             if (BIAS) {
-                const bool close = lane < got && lane + 1 < C && !(s.sorted[lane] - s.sorted[lane + 1] > 2.f * eps);
+                const float v0 = s.sorted[min(lane, got)], v1 = s.sorted[min(lane + 1, p.k)];
+                const bool close = lane < got && lane + 1 < C && !(v0 - v1 > 2.f * (eps + 0x1p-22f * fmaxf(fabsf(v0), fabsf(v1))));
                 if (__any_sync(all, close)) {
                     double sum64 = 0.0;
                     if (!p.sigmoid) {
@@ -362,11 +423,11 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
                     __syncwarp();
                     for (int c = lane; c < C; c += 32) {
                         const double v = s.exact[c];
-                        const uint32_t low = (uint32_t)s.key[c];  // larger: lower id
+                        const uint32_t inv_id = (uint32_t)s.key[c];  // larger: lower id
                         int place = 0;
                         for (int j = 0; j < C; ++j)
-                            place += s.exact[j] > v || (s.exact[j] == v && (uint32_t)s.key[j] > low) ? 1 : 0;
-                        if (place < p.k) s.id[place] = (int32_t)~low;
+                            place += s.exact[j] > v || (s.exact[j] == v && (uint32_t)s.key[j] > inv_id) ? 1 : 0;
+                        if (place < p.k) s.id[place] = (int32_t)~inv_id;
                     }
                     __syncwarp();
                 }
@@ -396,6 +457,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
         }
     }
     if (__syncthreads_or(unsettled)) {
+        GateExact &slow = *reinterpret_cast<GateExact *>(gate_raw);  // over the warps' parts, which are done with
         for (int w = 0; w < kGateWarps; ++w) {
             if (w == warp && unsettled) gate_exact(p, t, slow);
             __syncthreads();

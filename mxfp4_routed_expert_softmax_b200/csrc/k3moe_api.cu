@@ -857,7 +857,7 @@ k3moe_status check_linear(const k3moe_linear_desc *l) {
 template <int NI>
 cudaError_t launch_gate_ni(const GateParams &p, cudaStream_t st) {
     const dim3 grid((unsigned)ceil_div(p.T, kGateWarps)), block(32 * kGateWarps);
-    const size_t smem = gate_smem(p.E, p.groups);
+    const size_t smem = gate_smem(NI);
     return p.bias ? launch(gate_kernel<NI, true>, grid, block, smem, st, true, p)
                   : launch(gate_kernel<NI, false>, grid, block, smem, st, true, p);
 }
