@@ -279,28 +279,43 @@ __global__ void __launch_bounds__(kPfThreads, 1) pf_expert_kernel(const __grid_c
         int s = 0;
         uint32_t ph = 0u;
         uint32_t nanb = 0u;  // E8M0 NaN bytes met among the weight scales (strict mode)
-        for (int q = 0; q < nmine; ++q) {
-            const PfSlot *sl = slot_wait(q);
-            if (!sl) break;
-            const int it = item_of(q);
-            const bool shared = it >= IR;
-            const bool ok = sl->ok != 0;
-            const int rb = sl->rb;
-            const uint8_t *blob = (!shared && ok && !p.sf_tma) ? p.blobs[sl->eid] : nullptr;
-            const int nk = nk_of(it);
-            bool go = true;
-            for (int kt = 0; kt < nk; ++kt) {
-                if (!wait(&full[s], ph)) {
-                    go = false;
-                    break;
-                }
-                if (!shared) {
-                    const uint8_t *st = smem + s * SB;
-                    const uint32_t col = tbase + lb + sf0 + (uint32_t)(s * SFC);
+        // the B scales: column 4g + n/32, lane n%32
+        auto put_b = [&](const uint8_t *st, uint32_t col) {
+            const uint32_t *sb = reinterpret_cast<const uint32_t *>(st + pf_sfb_off(GU));
+            const uint32_t w[8] = {sb[lane],        sb[32 + lane],        sb[64 + lane],        sb[96 + lane],
+                                   sb[kPfN + lane], sb[kPfN + 32 + lane], sb[kPfN + 64 + lane], sb[kPfN + 96 + lane]};
+            umma::st8(col + 8 * NMAT, w);
+            umma::wait_st();
+        };
+        auto stage_done = [&] {
+            umma::fence_before();
+            __syncwarp();
+            if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&sfr[s])) : "memory");
+            if (++s == nst) {
+                s = 0;
+                ph ^= 1u;
+            }
+        };
+        if (p.sf_tma) {
+            for (int q = 0; q < nmine; ++q) {
+                const PfSlot *sl = slot_wait(q);
+                if (!sl) break;
+                const int it = item_of(q);
+                const bool shared = it >= IR;
+                const bool ok = sl->ok != 0;
+                const int nk = nk_of(it);
+                bool go = true;
+                for (int kt = 0; kt < nk; ++kt) {
+                    if (!wait(&full[s], ph)) {
+                        go = false;
+                        break;
+                    }
+                    if (!shared) {
+                        const uint8_t *st = smem + s * SB;
+                        const uint32_t col = tbase + lb + sf0 + (uint32_t)(s * SFC);
 #pragma unroll
-                    for (int m = 0; m < NMAT; ++m) {
-                        uint32_t w[8];
-                        if (p.sf_tma) {
+                        for (int m = 0; m < NMAT; ++m) {
+                            uint32_t w[8];
                             const uint8_t *sfa = st + pf_sfa_off(GU) + m * 2048 + (kt & 1) * 8;
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
@@ -310,41 +325,105 @@ __global__ void __launch_bounds__(kPfThreads, 1) pf_expert_kernel(const __grid_c
                                 w[j] = v.x;
                                 w[4 + j] = v.y;
                             }
-                        } else {
-                            const uint8_t *plane = nullptr;
-                            if (blob != nullptr)
-                                plane = GU ? (m == 0 ? blob + mat / 2 : blob + mat + mat / 32)
-                                           : blob + mat + mat / 16 + mat / 2;
-                            const int nks = min(4, (K - kt * kTileK) / 64);
+                            umma::st8(col + 8 * m, w);
+                        }
+                        put_b(st, col);
+                    }
+                    stage_done();
+                }
+                slot_done(q);
+                if (!go) break;
+            }
+        } else {
+            // Scale rows that TMA cannot address: each warp loads the 32 rows
+            // of its quadrant from global memory, kLook K-tiles ahead (into
+            // the next items where they are short), and the four exchange
+            // them through the stage.  A description is released only when
+            // its item is done, so looking ahead may hold all but one of them.
+            constexpr int kLook = 3;
+            static_assert(kLook < kPfSlots, "the item in work and kLook ahead");
+            uint2 ring[kLook][NMAT];
+            int aq = 0, akt = 0, ank = 0, arb = 0;  // the K-tile to load next
+            const uint8_t *ablob = nullptr;
+            bool ahead = true;
+            auto load = [&](uint2 (&r)[NMAT]) {
+                if (!ahead || aq >= nmine) return;
+                if (akt == 0) {
+                    const PfSlot *sl = slot_wait(aq);
+                    if (!sl) {
+                        ahead = false;
+                        return;
+                    }
+                    const int it = item_of(aq);
+                    ank = nk_of(it);
+                    arb = sl->rb;
+                    ablob = it < IR && sl->ok != 0 ? p.blobs[sl->eid] : nullptr;
+                }
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const int row = rb * kTileM + 32 * j + lane;
-                                uint2 v = make_uint2(0u, 0u);
-                                if (plane != nullptr && row < M) v = load_sf8(plane + (size_t)row * (K / 32) + kt * 8, nks);
-                                nanb |= e8m0_nan8(v.x, v.y);
-                                w[j] = v.x;
-                                w[4 + j] = v.y;
+                for (int m = 0; m < NMAT; ++m) {
+                    const int row = arb * kTileM + 32 * (warp & 3) + lane;
+                    uint2 v = make_uint2(0u, 0u);
+                    if (ablob != nullptr && row < M) {
+                        const uint8_t *plane = GU ? (m == 0 ? ablob + mat / 2 : ablob + mat + mat / 32)
+                                                  : ablob + mat + mat / 16 + mat / 2;
+                        v = load_sf8(plane + (size_t)row * (K / 32) + akt * 8, min(4, (K - akt * kTileK) / 64));
+                    }
+                    r[m] = v;
+                }
+                if (++akt == ank) {
+                    akt = 0;
+                    ++aq;
+                }
+            };
+#pragma unroll
+            for (int i = 0; i < kLook; ++i) load(ring[i]);
+            int q = 0, kt = 0;
+            bool go = true;
+            while (q < nmine && go) {
+#pragma unroll
+                for (int i = 0; i < kLook; ++i) {
+                    if (q < nmine && go) {
+                        const int it = item_of(q);
+                        bool ok = slot_wait(q) != nullptr;
+                        ok = ok && wait(&full[s], ph);
+                        uint2 *sx = reinterpret_cast<uint2 *>(smem + s * SB + pf_sfa_off(GU));  // [matrix][256]: 128 rows
+                        if (it < IR) {
+#pragma unroll
+                            for (int m = 0; m < NMAT; ++m) {
+                                nanb |= e8m0_nan8(ring[i][m].x, ring[i][m].y);
+                                sx[m * 256 + 32 * (warp & 3) + lane] = ring[i][m];
                             }
                         }
-                        umma::st8(col + 8 * m, w);
+                        __syncwarp();
+                        // the four warps go on together or not at all
+                        go = umma::bar_red_and(1, 128, ok);
+                        if (go) {
+                            if (it < IR) {
+                                const uint32_t col = tbase + lb + sf0 + (uint32_t)(s * SFC);
+#pragma unroll
+                                for (int m = 0; m < NMAT; ++m) {
+                                    uint32_t w[8];
+#pragma unroll
+                                    for (int j = 0; j < 4; ++j) {
+                                        const uint2 v = sx[m * 256 + 32 * j + lane];
+                                        w[j] = v.x;
+                                        w[4 + j] = v.y;
+                                    }
+                                    umma::st8(col + 8 * m, w);
+                                }
+                                put_b(smem + s * SB, col);
+                            }
+                            stage_done();
+                            load(ring[i]);
+                            if (++kt == nk_of(it)) {
+                                kt = 0;
+                                slot_done(q);
+                                ++q;
+                            }
+                        }
                     }
-                    // B scales: column 4g + n/32, lane n%32
-                    const uint32_t *sb = reinterpret_cast<const uint32_t *>(st + pf_sfb_off(GU));
-                    const uint32_t w[8] = {sb[lane],        sb[32 + lane],        sb[64 + lane],        sb[96 + lane],
-                                           sb[kPfN + lane], sb[kPfN + 32 + lane], sb[kPfN + 64 + lane], sb[kPfN + 96 + lane]};
-                    umma::st8(col + 8 * NMAT, w);
-                    umma::wait_st();
-                }
-                umma::fence_before();
-                __syncwarp();
-                if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&sfr[s])) : "memory");
-                if (++s == nst) {
-                    s = 0;
-                    ph ^= 1u;
                 }
             }
-            slot_done(q);
-            if (!go) break;
         }
         if (p.strict && __any_sync(0xffffffffu, nanb != 0u) && lane == 0) set_status(hdr, kStDeviceCheck);
     } else if (warp == 9) {

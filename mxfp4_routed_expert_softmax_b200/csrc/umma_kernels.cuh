@@ -275,6 +275,10 @@ __host__ __device__ inline int umma_smem_bytes(bool gu, int N, int nst) {
 // 2-byte pairs (one per MMA k-step); zero beyond.
 __device__ __forceinline__ uint2 load_sf8(const uint8_t *p, int nks) {
     if (nks == 4 && (reinterpret_cast<uintptr_t>(p) & 7u) == 0u) return __ldg(reinterpret_cast<const uint2 *>(p));
+    if (nks == 4 && (reinterpret_cast<uintptr_t>(p) & 3u) == 0u) {
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(p);
+        return make_uint2(__ldg(w), __ldg(w + 1));
+    }
     const unsigned short *h = reinterpret_cast<const unsigned short *>(p);
     uint32_t w0 = 0u, w1 = 0u;
     if (nks > 0) w0 |= (uint32_t)__ldg(h);
@@ -719,11 +723,14 @@ __global__ void __launch_bounds__(kUThreads, 1) umma_expert_kernel(const __grid_
         } else {
         // The global loads of a unit's scales are issued kLook units ahead of
         // its TMEM stores (a ring of registers), so their latency overlaps the
-        // pipeline instead of adding to every stage.  Shared (bf16) units have
-        // no scales: the warps only keep the stage protocol.
+        // pipeline instead of adding to every stage.  Each warp loads the 32
+        // rows of its quadrant (a row's bytes are a line of their own: all four
+        // loading all rows cost 4000 cycles a unit in the first-level cache)
+        // and the warps exchange them through the stage.  Shared (bf16) units
+        // have no scales: the warps only keep the stage protocol.
         constexpr int kLook = 3;
         struct SfRegs {
-            uint32_t a[NMAT][8];  // column 8m + 4g + j: group g, row block j
+            uint2 a[NMAT];        // this lane's row: k-steps 0, 1 and 2, 3
             uint32_t b[4];        // B scales: (g0, rows 0-31), (g0, 32-63), (g1, ...), (g1, ...)
             bool on;
         };
@@ -738,15 +745,11 @@ __global__ void __launch_bounds__(kUThreads, 1) umma_expert_kernel(const __grid_
                 const uint8_t *plane = nullptr;
                 if (blob != nullptr)
                     plane = GU ? (m == 0 ? blob + mat / 2 : blob + mat + mat / 32) : blob + mat + mat / 16 + mat / 2;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int row = x.rb * RB + (GU ? 0 : m * kTileM) + 32 * j + lane;
-                    uint2 v = make_uint2(0u, 0u);
-                    if (plane != nullptr && row < M) v = load_sf8(plane + (size_t)row * (K / 32) + x.kt * 8, nks);
-                    nanb |= e8m0_nan8(v.x, v.y);
-                    r.a[m][j] = v.x;      // group 0: k-steps 0, 1
-                    r.a[m][4 + j] = v.y;  // group 1: k-steps 2, 3
-                }
+                const int row = x.rb * RB + (GU ? 0 : m * kTileM) + 32 * (warp & 3) + lane;
+                uint2 v = make_uint2(0u, 0u);
+                if (plane != nullptr && row < M) v = load_sf8(plane + (size_t)row * (K / 32) + x.kt * 8, nks);
+                nanb |= e8m0_nan8(v.x, v.y);
+                r.a[m] = v;
             }
             const uint32_t *sfb = GU ? reinterpret_cast<const uint32_t *>(p.ws + L.xsf) + (size_t)x.kt * 2 * kSfRow
                                      : reinterpret_cast<const uint32_t *>(p.ws + L.hsf) +
@@ -758,14 +761,28 @@ __global__ void __launch_bounds__(kUThreads, 1) umma_expert_kernel(const __grid_
         };
         auto store = [&](int it, const SfRegs &r) {
             const int s = it % nst;
-            // lane 0 decides, the warp follows (the TMEM stores are warp-collective)
-            int go = 0;
-            if (lane == 0) go = it < nst ? !*s_abort : wait(&empty[s], (uint32_t)(((it / nst) + 1) & 1));
-            if (!__shfl_sync(0xffffffffu, go, 0)) return false;
+            uint2 *sx = reinterpret_cast<uint2 *>(smem + s * SB + umma_sfa_off(GU, N));  // [matrix][256]: 128 rows
+            bool ok = it < nst || mbar_wait_warp(&empty[s], (uint32_t)(((it / nst) + 1) & 1), hdr, p.wait_ns, s_abort);
+            if (r.on) {
+#pragma unroll
+                for (int m = 0; m < NMAT; ++m) sx[m * 256 + 32 * (warp & 3) + lane] = r.a[m];
+            }
+            __syncwarp();
+            // the four warps go on together or not at all
+            if (!umma::bar_red_and(2, 128, ok)) return false;
             if (r.on) {
                 const uint32_t col = tbase + lb + sf0 + (uint32_t)(s * SFC);
 #pragma unroll
-                for (int m = 0; m < NMAT; ++m) umma::st8(col + 8 * m, r.a[m]);
+                for (int m = 0; m < NMAT; ++m) {
+                    uint32_t w[8];  // column 8m + 4g + j: group g, row block j
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint2 v = sx[m * 256 + 32 * j + lane];
+                        w[j] = v.x;
+                        w[4 + j] = v.y;
+                    }
+                    umma::st8(col + 8 * m, w);
+                }
                 const uint32_t w[8] = {r.b[0], r.b[1], 0u, 0u, r.b[2], r.b[3], 0u, 0u};
                 umma::st8(col + 8 * NMAT, w);
                 umma::wait_st();
