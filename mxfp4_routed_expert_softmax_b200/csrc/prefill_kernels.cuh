@@ -346,13 +346,13 @@ __global__ void __launch_bounds__(kRouteThreads) pf_prep_kernel(const __grid_con
             for (int q = 0; q < 4; ++q) r[8 * h + 2 * q] = bf16_lo(w[q]), r[8 * h + 2 * q + 1] = bf16_hi(w[q]);
         }
         uint2 code[kPfPieces];
-        uint32_t exps;
+        uint32_t exps[1];
         quantize_pieces_half<kPfPieces>(r, code, exps);
         if (c0 < 8) {
 #pragma unroll
             for (int pc = 0; pc < kPfPieces; ++pc) {
                 *reinterpret_cast<uint2 *>(&stage[wl][c0][pc][8 * half]) = code[pc];
-                if (half == 0) sstage[wl][c0 >> 2][pc][c0 & 3] = c0 < nbk ? (uint8_t)(exps >> (8 * pc)) : (uint8_t)0;
+                if (half == 0) sstage[wl][c0 >> 2][pc][c0 & 3] = c0 < nbk ? (uint8_t)(exps[0] >> (8 * pc)) : (uint8_t)0;
             }
         }
         if (p.ngs > 0 && c0 < nbk) {

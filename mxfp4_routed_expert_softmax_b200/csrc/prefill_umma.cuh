@@ -584,7 +584,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) pf_expert_kernel(const __grid_c
 #pragma unroll
                                 for (int i = 0; i < 16; ++i) r[i] = hx[j * kPfHx + 16 * half + i];
                                 uint2 code[kPfPieces];
-                                uint32_t exps;
+                                uint32_t exps[1];
                                 quantize_pieces_half<kPfPieces>(r, code, exps);
                                 const int row0 = (t0 + j) * kPfPieces;  // B rows of the token's pieces
                                 uint8_t *dst = tile + c * (kPfN / 8) * 128 + (row0 / 8) * 128 + (row0 % 8) * 16 + 8 * half;
@@ -592,7 +592,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) pf_expert_kernel(const __grid_c
                                 for (int pc = 0; pc < kPfPieces; ++pc) {
                                     *reinterpret_cast<uint2 *>(dst + pc * 16) = code[pc];
                                     if (half == 0)
-                                        sfw[((c >> 2) * kPfN + row0 + pc) * 4 + (c & 3)] = (uint8_t)(exps >> (8 * pc));
+                                        sfw[((c >> 2) * kPfN + row0 + pc) * 4 + (c & 3)] = (uint8_t)(exps[0] >> (8 * pc));
                                 }
                                 __syncwarp();
                             }

@@ -100,11 +100,11 @@ __device__ __forceinline__ void quantize_pieces_t(float v, int lane, int t, int 
 // an element per lane the warp-wide steps waited for one another: 430 cycles
 // for a block's piece, against about 25 here (32 blocks at a time).
 // out[p]: this half's 8 code bytes of piece p; exps: the pieces' scale bytes,
-// piece p in byte p.
+// piece p in byte p % 4 of word p / 4.
 template <int P>
-__device__ __forceinline__ void quantize_pieces_half(float (&r)[16], uint2 (&out)[P], uint32_t &exps) {
-    static_assert(P <= 4, "one byte per piece");
-    exps = 0u;
+__device__ __forceinline__ void quantize_pieces_half(float (&r)[16], uint2 (&out)[P], uint32_t (&exps)[(P + 3) / 4]) {
+#pragma unroll
+    for (int i = 0; i < (P + 3) / 4; ++i) exps[i] = 0u;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
         uint32_t bits = 0u;
@@ -143,7 +143,7 @@ __device__ __forceinline__ void quantize_pieces_half(float (&r)[16], uint2 (&out
             }
         }
         out[p] = make_uint2(w[0], w[1]);
-        exps |= (uint32_t)(e + 127) << (8 * p);
+        exps[p / 4] |= (uint32_t)(e + 127) << (8 * (p % 4));
     }
 }
 
@@ -267,8 +267,9 @@ __host__ __device__ inline int umma_sf_cols(bool) { return 32; }
 constexpr int kMetaU = kChunk * 32;  // distinct experts of a chunk (top_k <= 32)
 constexpr int kMetaBytes = kMetaU * 8 + kMetaU * 4 + kMetaU * kChunk * 4;
 constexpr int kUBarBytes = 512;  // mbarriers, the TMEM address and flags after the stages
+constexpr int kUHx = 33;  // floats from token to token where h changes from a row to a token per lane
 __host__ __device__ inline int umma_smem_bytes(bool gu, int N, int nst) {
-    return 1024 + nst * umma_stage_bytes(gu, N) + kUBarBytes + kMetaBytes;
+    return 1024 + nst * umma_stage_bytes(gu, N) + kUBarBytes + kMetaBytes + (gu ? 4 * kChunk * kUHx * 4 : 0);
 }
 
 // Load the (up to) 8 scale bytes of one weight row for one K-tile: nks valid
@@ -319,6 +320,7 @@ __global__ void __launch_bounds__(kUThreads, 1) umma_expert_kernel(const __grid_
     const uint8_t **s_blob = reinterpret_cast<const uint8_t **>(smem + nst * SB + kUBarBytes);
     int32_t *s_eid = reinterpret_cast<int32_t *>(s_blob + kMetaU);
     float *s_wu = reinterpret_cast<float *>(s_eid + kMetaU);  // [u][t]
+    float *s_hx = s_wu + kMetaU * kChunk;                      // gate/up: [warp][token][kUHx]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Layout &L = p.L;
     WsHeader *hdr = reinterpret_cast<WsHeader *>(p.ws + L.hdr);
@@ -992,14 +994,44 @@ __global__ void __launch_bounds__(kUThreads, 1) umma_expert_kernel(const __grid_
                         const int kt = blk >> 3;
                         uint8_t *tile = p.ws + L.hb + ((size_t)x.u * nkt_ff + kt) * N * 128;
                         uint8_t *sfw = p.ws + L.hsf + ((size_t)x.u * nkt_ff + kt) * 2 * kSfRow * 4;
+                        // One token: an element per lane as it is (81 us for
+                        // the layer's 16 of 64 experts with the exchange, 79
+                        // without).  More: through shared memory, so that
+                        // lanes t and t + 16 hold the two halves of token t's
+                        // block (8 tokens: 207 us, 221 one by one).
+                        float *hx = s_hx + warp * kChunk * kUHx;
 #pragma unroll
                         for (int t = 0; t < kChunk; ++t) {
                             if (t < Tc) {
                                 float h = 0.f;
                                 const float w = s_wu[x.u * kChunk + t];
                                 if (blob != nullptr && w != 0.f && f < p.ff) h = silu_mul(acc[0][t], acc[1][t]) * w;
-                                quantize_pieces(h, lane, t, blk & 7, N, tile, sfw);
+                                if (t == 0 && Tc == 1)
+                                    quantize_pieces(h, lane, 0, blk & 7, N, tile, sfw);
+                                else
+                                    hx[t * kUHx + lane] = h;
                             }
+                        }
+                        __syncwarp();
+                        if (Tc > 1) {
+                        const int t = lane & 15, half = lane >> 4, c = blk & 7;
+                        float r[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) r[i] = t < Tc ? hx[t * kUHx + 16 * half + i] : 0.f;
+                        uint2 code[kPieces];
+                        uint32_t exps[(kPieces + 3) / 4];
+                        quantize_pieces_half<kPieces>(r, code, exps);
+                        if (t < Tc) {
+#pragma unroll
+                            for (int pc = 0; pc < kPieces; ++pc) {
+                                const int n = t * kPieces + pc;
+                                *reinterpret_cast<uint2 *>(tile + c * (N / 8) * 128 + (n / 8) * 128 + (n % 8) * 16 + 8 * half) =
+                                    code[pc];
+                                if (half == 0)
+                                    sfw[((c >> 2) * kSfRow + n) * 4 + (c & 3)] = (uint8_t)(exps[pc / 4] >> (8 * (pc % 4)));
+                            }
+                        }
+                        __syncwarp();
                         }
                     } else if (f < p.ffs) {
                         // shared: h as bf16 hi + lo (pieces 0, 1; the others zero), weight 1
