@@ -480,7 +480,7 @@ cudaError_t launch_given(const DeviceInfo &di, const RouteParams &rp, const Give
     if (grid > di.sms) grid = di.sms;
     *grid_out = grid;
     const GivenParams gp{rp, g.idx, g.weight};
-    return launch(given_setup_kernel, dim3(grid), dim3(kGivenThreads), 0, st, false, gp);
+    return launch(given_setup_kernel, dim3(grid), dim3(kGivenThreads), 0, st, true, gp);
 }
 
 // Launches of the grouped prefill, pass after pass; rp carries the shapes,
@@ -544,7 +544,7 @@ k3moe_status prefill_impl(DeviceInfo &di, RouteParams rp, const k3moe_dims *dims
                                    reinterpret_cast<float *>(wsb + P.wt),
                                    reinterpret_cast<WsHeader *>(wsb + rp.L.hdr)};
             const int per = kGivenThreads / 32;
-            e = launch(pf_given_kernel, dim3(ceil_div(Tq, per)), dim3(kGivenThreads), 0, st, false, gp);
+            e = launch(pf_given_kernel, dim3(ceil_div(Tq, per)), dim3(kGivenThreads), 0, st, true, gp);
             if (e != cudaSuccess) return cuda_fail(e, "given routing launch");
         } else {
             // router: tiles of 128 experts x 128 tokens on the tensor cores
@@ -561,11 +561,11 @@ k3moe_status prefill_impl(DeviceInfo &di, RouteParams rp, const k3moe_dims *dims
         }
         if (routing_only) continue;
         const int nhb = ceil_div(Tq, kPfHistTok);
-        e = launch(pf_hist_kernel, dim3(nhb), dim3(kRouteThreads), 0, st, false, pp);
-        if (e == cudaSuccess) e = launch(pf_scan_kernel, dim3(1), dim3(kPfScanThreads), 0, st, false, pp);
-        if (e == cudaSuccess) e = launch(pf_place_kernel, dim3(nhb), dim3(kRouteThreads), 0, st, false, pp);
-        if (e == cudaSuccess) e = launch(pf_items_kernel, dim3(2 * di.sms), dim3(256), 0, st, false, pp);
-        if (e == cudaSuccess) e = launch(pf_prep_kernel, dim3(2 * di.sms), dim3(kRouteThreads), 0, st, false, pp);
+        e = launch(pf_hist_kernel, dim3(nhb), dim3(kRouteThreads), 0, st, true, pp);
+        if (e == cudaSuccess) e = launch(pf_scan_kernel, dim3(1), dim3(kPfScanThreads), 0, st, true, pp);
+        if (e == cudaSuccess) e = launch(pf_place_kernel, dim3(nhb), dim3(kRouteThreads), 0, st, true, pp);
+        if (e == cudaSuccess) e = launch(pf_items_kernel, dim3(2 * di.sms), dim3(256), 0, st, true, pp);
+        if (e == cudaSuccess) e = launch(pf_prep_kernel, dim3(2 * di.sms), dim3(kRouteThreads), 0, st, true, pp);
         if (e != cudaSuccess) return cuda_fail(e, "prefill dispatch launch");
         PfUmmaParams up{};
         up.d = d;
@@ -601,7 +601,7 @@ k3moe_status prefill_impl(DeviceInfo &di, RouteParams rp, const k3moe_dims *dims
         cp.y = reinterpret_cast<uint8_t *>(y) + (size_t)t0 * d * (out32 ? 4 : 2);
         cp.resid = norm_w ? x + (size_t)t0 * d : nullptr;
         cp.idx = given ? reinterpret_cast<const int32_t *>(wsb + P.idx) : nullptr;
-        e = launch(pf_combine_kernel, dim3(4 * di.sms), dim3(256), 0, st, false, cp);
+        e = launch(pf_combine_kernel, dim3(4 * di.sms), dim3(256), 0, st, true, cp);
         if (e != cudaSuccess) return cuda_fail(e, "prefill combine launch");
     }
     return K3MOE_OK;

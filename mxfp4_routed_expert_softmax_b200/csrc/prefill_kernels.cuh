@@ -168,6 +168,8 @@ __global__ void __launch_bounds__(kRouteThreads) pf_topk_kernel(const __grid_con
 // group (one CTA); (3) each pair's position = expert start + block prefix +
 // pairs of the same expert at earlier tokens of its block.
 __global__ void __launch_bounds__(kRouteThreads) pf_hist_kernel(const __grid_constant__ PfRouteParams p) {
+    pdl_wait();
+    pdl_trigger();
     __shared__ uint32_t h[1024];
     const int E = p.r.E, k = p.r.k;
     for (int e = threadIdx.x; e < E; e += blockDim.x) h[e] = 0u;
@@ -186,6 +188,8 @@ __global__ void __launch_bounds__(kRouteThreads) pf_hist_kernel(const __grid_con
 constexpr int kPfScanThreads = 1024;
 
 __global__ void __launch_bounds__(kPfScanThreads) pf_scan_kernel(const __grid_constant__ PfRouteParams p) {
+    pdl_wait();
+    pdl_trigger();
     __shared__ uint32_t s_tot[32];
     const int E = p.r.E, e = threadIdx.x, nhb = ceil_div(p.T, kPfHistTok);
     uint8_t *ws = p.r.ws;
@@ -245,6 +249,8 @@ __global__ void __launch_bounds__(kPfScanThreads) pf_scan_kernel(const __grid_co
 }
 
 __global__ void __launch_bounds__(kRouteThreads) pf_place_kernel(const __grid_constant__ PfRouteParams p) {
+    pdl_wait();
+    pdl_trigger();
     __shared__ int32_t s_idx[kPfHistTok * 32];
     const int E = p.r.E, k = p.r.k;
     const int t0 = blockIdx.x * kPfHistTok, t1 = min(p.T, t0 + kPfHistTok);
@@ -279,6 +285,8 @@ __global__ void __launch_bounds__(kRouteThreads) pf_place_kernel(const __grid_co
 // groups last.  Entry: (group | row block << 20, expert or -1, first position
 // or token, tokens | blob ok << 8).  One thread per (group, row block).
 __global__ void pf_items_kernel(const __grid_constant__ PfRouteParams p) {
+    pdl_wait();
+    pdl_trigger();
     const uint8_t *ws = p.r.ws;
     const int NG = (int)*reinterpret_cast<const volatile uint32_t *>(
         &reinterpret_cast<const WsHeader *>(ws + p.r.L.hdr)->n_unique);
@@ -316,6 +324,8 @@ __global__ void pf_items_kernel(const __grid_constant__ PfRouteParams p) {
 constexpr int kPrepWarps = kRouteThreads / 32;
 
 __global__ void __launch_bounds__(kRouteThreads) pf_prep_kernel(const __grid_constant__ PfRouteParams p) {
+    pdl_wait();
+    pdl_trigger();
     __shared__ __align__(16) uint8_t stage[kPrepWarps][8][kPfPieces][16];
     __shared__ __align__(16) uint8_t sstage[kPrepWarps][2][kPfPieces][4];
     const int lane = threadIdx.x & 31, wl = threadIdx.x >> 5, d = p.r.d, k = p.r.k;
@@ -417,21 +427,40 @@ struct PfCombineParams {
 };
 
 __global__ void pf_combine_kernel(const __grid_constant__ PfCombineParams p) {
+    pdl_wait();
+    pdl_trigger();
     const int nq = p.d / 4;
     const size_t n = (size_t)p.T * nq;
     for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (size_t)gridDim.x * blockDim.x) {
         const size_t t = i / nq, q = i - t * nq;
         const float4 *src = reinterpret_cast<const float4 *>(p.o + t * (size_t)(p.k + 1) * p.d) + q;
         const int32_t *id = p.idx ? p.idx + t * p.k : nullptr;
-        float4 s = id && id[0] < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : __ldcs(src);
-        const int ns = p.k + (p.has_shared ? 1 : 0);
-        for (int j = 1; j < ns; ++j) {
-            if (id && j < p.k && id[j] < 0) continue;
-            const float4 v = __ldcs(src + (size_t)j * nq);
-            s.x += v.x;
-            s.y += v.y;
-            s.z += v.z;
-            s.w += v.w;
+        const int ns = p.k + (p.has_shared ? 1 : 0);  // at most 33
+        uint64_t there = ~0ull;
+        if (id) {
+            for (int j = 0; j < p.k; ++j)
+                if (id[j] < 0) there &= ~(1ull << j);
+        }
+        // eight slots' loads in flight at a time, added in slot order
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j0 = 0; j0 < ns; j0 += 8) {
+            float4 v[8];
+#pragma unroll
+            for (int i8 = 0; i8 < 8; ++i8)
+                if (j0 + i8 < ns && ((there >> (j0 + i8)) & 1ull)) v[i8] = __ldcs(src + (size_t)(j0 + i8) * nq);
+#pragma unroll
+            for (int i8 = 0; i8 < 8; ++i8) {
+                if (j0 + i8 < ns && ((there >> (j0 + i8)) & 1ull)) {
+                    if (j0 + i8 == 0) {
+                        s = v[0];
+                    } else {
+                        s.x += v[i8].x;
+                        s.y += v[i8].y;
+                        s.z += v[i8].z;
+                        s.w += v[i8].w;
+                    }
+                }
+            }
         }
         if (p.resid) {
             const uint2 hv = *reinterpret_cast<const uint2 *>(p.resid + 4 * i);

@@ -62,7 +62,11 @@ __global__ void __launch_bounds__(kGivenThreads) given_setup_kernel(const __grid
     WsHeader *hdr = reinterpret_cast<WsHeader *>(r.ws + L.hdr);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int nwc = kGivenThreads / 32;
-    pdl_trigger();  // the gate/up pass waits for what it reads: x on prep_done, the rest on this grid
+    // The gate/up pass, which may start now, waits for what it reads: x on
+    // prep_done, the rest on this grid.  First this grid waits itself: the
+    // counters of the previous call are then back at zero.
+    pdl_wait();
+    pdl_trigger();
     if (blockIdx.x > 0 || gridDim.x == 1) {
         const int b0 = gridDim.x == 1 ? 0 : 1;
         build_x_pieces(r.x, r.Tc, r.d, r.ws, L, (blockIdx.x - b0) * nwc + warp, (gridDim.x - b0) * nwc,
@@ -146,6 +150,8 @@ struct PfGivenParams {
     WsHeader *hdr;
 };
 __global__ void __launch_bounds__(kGivenThreads) pf_given_kernel(const __grid_constant__ PfGivenParams p) {
+    pdl_wait();
+    pdl_trigger();
     const int lane = threadIdx.x & 31;
     const int t = blockIdx.x * (kGivenThreads / 32) + (threadIdx.x >> 5);
     if (t >= p.T) return;
