@@ -358,6 +358,8 @@ k3moe_status k3moe_layer_routed(const void *x, int32_t T, const int32_t *idx, co
  * act: K3MOE_ACT_NONE, _RELU, _SILU (v / (1 + exp(-v))), _GELU (v times the
  * normal distribution function of v), _GELU_TANH (its tanh approximation).
  * Products are exact, sums and the epilogue fp32, one rounding at the end.
+ * One launch; the variant (and with it the order of the sums) depends on T, n,
+ * k, the gate and the output's type, never on the values.
  *
  * x: bf16, T rows of k elements, ldx elements from row to row; w, w_gate:
  *   bf16, n rows of k elements, ldw from row to row (both alike); bias,
@@ -366,10 +368,10 @@ k3moe_status k3moe_layer_routed(const void *x, int32_t T, const int32_t *idx, co
  *   bf16 or fp32 with K3MOE_OUT_FP32, ldo.  A row distance of 0 means rows
  *   without gaps.  residual may be out itself (in place, ldr == ldo); no
  *   other overlap with out is allowed.
- * 1 <= n, 8 <= k, both at most 2^24; k, ldx and ldw multiples of 8; x, w and
- *   w_gate 16-byte aligned; bias, bias_gate 4-byte aligned; residual and out
- *   aligned to their element size (16-byte aligned rows are stored and read
- *   with wider accesses).
+ * 1 <= n, 8 <= k, both at most 2^24, T at most 2^30; k, ldx and ldw multiples
+ *   of 8; x, w and w_gate 16-byte aligned; bias, bias_gate 4-byte aligned;
+ *   residual and out aligned to their element size (16-byte aligned rows are
+ *   stored and read with wider accesses).
  * ws: device scratch of k3moe_linear_workspace_size() bytes for the call's T
  *   or a larger one, 256-byte aligned and zero-filled before its first use;
  *   it starts with a status word for k3moe_device_status, and must not be

@@ -1,7 +1,10 @@
 """Python binding of libk3moe.so, the B200 (sm_100a) MXFP4 routed-expert MoE
 layer.  Argument marshalling only: torch tensors supply device memory and
 streams, every step of the layer runs in the library's CUDA kernels.  The
-C contract of each call is documented in include/k3moe.h.
+C contract of each call is documented in include/k3moe.h.  k3moe_gate,
+k3moe_linear and k3moe_layer_routed go through a compiled module
+(csrc/py_binding.cpp), which refuses tensors that are not in the current
+device's memory; the other calls go through ctypes.
 
 The library is loaded at import time; if it has not been built (``python
 mxfp4_routed_expert_softmax_b200/build.py``) the import fails loudly -- there is

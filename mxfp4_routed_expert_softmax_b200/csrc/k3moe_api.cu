@@ -988,7 +988,7 @@ k3moe_status linear_launch(const LinearParams &p, WsHeader *hdr, cudaStream_t st
     }
     a.nrb = nrb;
     bool pair = false;
-    if (!p.out_fp32) {
+    if (!p.out_fp32 && di->pairs > 0) {
         const int nrb2 = ceil_div(nrb, 2);
         for (int bn = 64; bn <= 256; bn += 32) {
             const int ntt = ceil_div(p.T, bn);

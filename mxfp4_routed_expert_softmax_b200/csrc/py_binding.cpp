@@ -3,6 +3,7 @@
 // like the ctypes wrappers of the other calls, but read from the tensors
 // without a Python call each: through ctypes a call cost 10 to 13 us of host
 // time, more than most of its kernels take.
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -41,6 +42,19 @@ int64_t rows(PyObject *o, size_t size, int64_t cols) {
         return -1;
     if (dim == 1 || t->size(0) == 1) return cols;
     return t->stride(0) >= cols ? t->stride(0) : -1;
+}
+
+// Whether every tensor among the arguments is in the current device's memory
+// (the library runs on that device and takes the addresses as they are).
+bool on_device(PyObject *const *a, Py_ssize_t n) {
+    int device = -1;
+    for (Py_ssize_t i = 0; i < n; ++i)
+        if (const at::Tensor *t = tensor_of(a[i])) {
+            if (!t->is_cuda()) return false;
+            if (device < 0) device = c10::cuda::current_device();
+            if (t->device().index() != device) return false;
+        }
+    return true;
 }
 
 // Whether a tensor is contiguous with elements of 4 bytes.
@@ -130,7 +144,7 @@ PyObject *gate(PyObject *, PyObject *const *a, Py_ssize_t n) {
         !address(a[4], &idx) || !address(a[5], &weight) || !stream_of(a[6], &stream))
         return nullptr;
     const int64_t ld = rows(a[0], d->flags & K3MOE_LOGITS_BF16 ? 2 : 4, d->n_experts);
-    if (ld < 0 || !flat4(a[2]) || !flat4(a[4]) || !flat4(a[5])) return status(K3MOE_ERR_INVALID_ARGUMENT);
+    if (!on_device(a, 6) || ld < 0 || !flat4(a[2]) || !flat4(a[4]) || !flat4(a[5])) return status(K3MOE_ERR_INVALID_ARGUMENT);
     return call(g_gate, logits, ld, T, static_cast<const float *>(bias), d, static_cast<int32_t *>(idx),
                 static_cast<float *>(weight), stream);
 }
@@ -147,7 +161,7 @@ PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
         return nullptr;
     const size_t osz = d->flags & K3MOE_OUT_FP32 ? 4 : 2;
     const int64_t ldx = rows(a[0], 2, d->k), ldw = rows(a[2], 2, d->k), ldr = rows(a[6], osz, d->n), ldo = rows(a[8], osz, d->n);
-    if (ldx < 0 || ldw < 0 || ldr < 0 || ldo < 0 || !flat4(a[4]) || !flat4(a[5]) ||
+    if (!on_device(a, 10) || ldx < 0 || ldw < 0 || ldr < 0 || ldo < 0 || !flat4(a[4]) || !flat4(a[5]) ||
         (a[3] != Py_None && rows(a[3], 2, d->k) != ldw))
         return status(K3MOE_ERR_INVALID_ARGUMENT);
     return call(g_linear, x, ldx, T, w, wg, ldw, static_cast<const float *>(b), static_cast<const float *>(bg), r, ldr, d, out,
@@ -165,7 +179,7 @@ PyObject *layer_routed(PyObject *, PyObject *const *a, Py_ssize_t n) {
         !descriptor(a[8], &d) || !address(a[9], &y) || !address(a[10], &ws) || !bytes_of(a[10], a[11], &bytes) ||
         !stream_of(a[12], &stream))
         return nullptr;
-    if (!flat4(a[2]) || !flat4(a[3])) return status(K3MOE_ERR_INVALID_ARGUMENT);
+    if (!on_device(a, 11) || !flat4(a[2]) || !flat4(a[3])) return status(K3MOE_ERR_INVALID_ARGUMENT);
     return call(g_routed, x, T, static_cast<const int32_t *>(idx), static_cast<const float *>(weight),
                 static_cast<const uint8_t *const *>(blobs), sg, su, sd, d, y, ws, bytes, stream);
 }

@@ -159,6 +159,55 @@ def test_masks(score, biased, groups, kept, group_top):
     compare(lb, k, b, **kw)
 
 
+def vector_ref(l, k, bias, sigmoid):
+    """The picks of many tokens at once, in 64 bits: sorts that keep the order of equal values."""
+    l = l.double()
+    c = (torch.sigmoid(l) if sigmoid else torch.softmax(l, 1)) + bias.double()
+    top, idx = c.sort(dim=1, descending=True, stable=True)
+    return torch.where(top[:, :k] > -np.inf, idx[:, :k], -1).to(torch.int32), c
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("kind", ["spread", "zero", "tiny", "masked", "huge", "coarse", "saturated"])
+def test_biased_picks_of_many_tokens(score, kind):
+    """Where the biased scores are told apart in 32 bits, where only 64 bits
+    do, and where there are more candidates than the list holds."""
+    T, E, k = 3000, 896, 16
+    l = logits(T, E, 77, torch.bfloat16 if kind in ("zero", "coarse") else torch.float32)
+    b = {"spread": biases(E, 3), "zero": torch.zeros(E, device="cuda"), "tiny": biases(E, 3, 1e-7),
+         "masked": biases(E, 3), "huge": biases(E, 3, 1e6), "coarse": torch.round(biases(E, 3, 1.0)),
+         "saturated": biases(E, 3, 1e-9)}[kind]
+    if kind == "masked":
+        b[::3] = -float("inf")
+    if kind == "coarse":
+        l = torch.round(l)
+    if kind == "saturated":
+        l = l.abs() * 4 + 14
+    idx, w = run(l, k, b, score=score)
+    ri, c = vector_ref(l, k, b, score == "sigmoid")
+    got = torch.as_tensor(idx, device="cuda")
+    # torch's exponentials and sums may differ from the definition's in the
+    # last bit of 64: a few units of the sum of score and bias
+    a = c.gather(1, got.clamp(min=0).long())
+    e = c.gather(1, ri.clamp(min=0).long())
+    gap = (a - e).abs() > 2.0 ** -48 * (1 + e.abs())
+    assert not bool((gap & (got != ri)).any())
+    assert float((got != ri).float().mean()) < (1e-3 if kind not in ("saturated", "tiny", "huge") else 2e-2)
+
+
+def test_small_scores_keep_their_ratios():
+    """Scores far below fp32's range, renormalised: the ratios of the formula."""
+    E, k = 96, 6
+    l = logits(20, E, 3) - 120.0
+    compare(l, k, None, score="sigmoid", renorm=True)
+    b = torch.where(torch.arange(E, device="cuda") < 20, 5.0, 0.0)  # picks the bias makes, with scores near 0
+    l = logits(20, E, 4)
+    l[:, :20] -= 150.0
+    compare(l, k, b, score="softmax", renorm=True)
+    compare(l, k, b, score="sigmoid", renorm=True)
+    compare(l, k, b, score="sigmoid")
+
+
 def test_row_distance_and_rows_behind():
     """Logits as a slice of wider rows; nothing behind the last row is written."""
     T, E, k = 19, 250, 9

@@ -74,6 +74,26 @@ def test_against_the_oracle(orc, cfg, T, ws_tokens, missing, shared):
     assert err.max() <= G1_TOL, err
 
 
+SCALES = [k3gen.Config("rows22", d=704, ff=192, E=48, k=8, ff_shared=64, T=0),    # scale rows of 22 and 6 bytes
+          k3gen.Config("rows20", d=640, ff=384, E=48, k=8, ff_shared=128, T=0),   # 20 and 12
+          k3gen.Config("rows24", d=768, ff=256, E=48, k=8, ff_shared=64, T=0),    # 24 and 8
+          k3gen.Config("rows2", d=1216, ff=64, E=48, k=8, ff_shared=64, T=0)]     # 38 and 2
+
+
+@pytest.mark.parametrize("cfg", SCALES, ids=lambda c: c.name)
+@pytest.mark.parametrize("T", [1, 2, 5, 8, 9, 60, 400])
+def test_scale_rows_of_every_alignment(orc, cfg, T):
+    """Reduction lengths whose scale rows no tensor map reaches, with several
+    items and several expert groups per CTA."""
+    W = kdev.weights(cfg)
+    inp = kdev.DeviceInputs(cfg, T=T)
+    idx, w = random_routing(cfg, T, T + 1, 0.1)
+    y = routed(cfg, W, inp.x, idx, w, m.K3MOE_OUT_FP32).cpu().numpy()
+    tokens = sample_tokens(T, 12)
+    err = g1_error(y[tokens], oracle_y(orc, cfg, W, inp.x_host, idx, w, tokens))
+    assert err.max() <= G1_TOL, err
+
+
 @pytest.mark.parametrize("cfg,T", [(TINY, 1), (SMALL, 8), (SMALL, 100), (k3gen.CONFIGS["k3_decode"], 1),
                                    (k3gen.CONFIGS["k3_decode"], 3)])
 def test_the_layers_own_routing_gives_the_layer(cfg, T):

@@ -106,6 +106,49 @@ def test_layer_sizes(T, n, k, gated, act, resid, fp32):
     assert torch.equal(a, b)  # the same inputs, the same bits
 
 
+@pytest.mark.parametrize("T,n,k,gated,act,resid,fp32", [
+    # rings that go round, and CTAs that go from group to group of columns
+    (3, 5000, 320, False, "none", True, False), (5, 4803, 4104, False, "relu", False, True),
+    (8, 3001, 1032, True, "silu", True, False), (1, 20000, 64, False, "gelu", False, False),
+    (2, 40, 30000, False, "none", True, True), (8, 17, 20008, True, "silu", False, True),
+    (12, 5001, 520, True, "gelu_tanh", False, False), (16, 2600, 1000, False, "none", True, False),
+    (9, 9001, 72, False, "relu", False, True),
+    # split reductions, chains longer than one
+    (17, 896, 7168, False, "none", False, True), (40, 130, 20000, False, "gelu", True, True),
+    (300, 64, 16384, False, "none", False, True), (100, 1536, 7168, True, "silu", False, False),
+    (129, 65, 9000, True, "silu", True, True), (500, 129, 2504, False, "relu", True, False),
+    # CTA pairs: ragged rows, columns and K
+    (1500, 3001, 520, True, "silu", True, False), (2047, 1000, 328, False, "none", False, False),
+    (1111, 2500, 1000, False, "gelu", True, False), (5000, 130, 2056, True, "relu", False, False),
+    (4096, 4104, 72, False, "none", True, False)])
+def test_variants(T, n, k, gated, act, resid, fp32):
+    check(data(T, n, k, T + n, gated, bias=n % 2 == 0, resid=resid, fp32=fp32), act, fp32)
+
+
+def test_first_call_is_captured():
+    """The library's set-up on a device happens in whichever call comes first,
+    also one that is captured."""
+    import subprocess
+    import sys
+    code = """
+import torch, mxfp4_routed_expert_softmax_b200 as m
+for T in (2, 40, 600):
+    x, w = torch.randn(T, 512, device="cuda").bfloat16(), torch.randn(256, 512, device="cuda").bfloat16()
+    lin = m.make_linear(256, 512, 0, m.K3MOE_OUT_FP32)
+    ws, out = m.new_linear_workspace(lin, T), torch.zeros(T, 256, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        m.check(m.k3moe_linear(x, T, w, None, None, None, None, lin, out, ws))
+    g.replay()
+    torch.cuda.synchronize()
+    ref = x.double() @ w.double().T
+    assert float((out.double() - ref).norm() / ref.norm()) < 1e-5
+print("captured")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
 def test_fp32_precision():
     """Long reductions with fp32 output stay within a few units of fp32: the
     partial sums are short enough that the error does not grow with K (a plain

@@ -72,6 +72,7 @@ def test_linear_rejects_bad_arguments(m):
         assert call(**bad) == INVALID, bad
     assert call(wsb=16) == WORKSPACE
     assert call(wsb=m.k3moe_linear_workspace_size(d, 1) - 1) == WORKSPACE
+    assert call(T=(1 << 30) + 1) == SHAPE
 
 
 def test_linear_workspace_covers_every_smaller_call(m):
@@ -103,6 +104,41 @@ def test_binding_rejects_wrong_tensors(m):
         assert m.k3moe_linear(a["x"], 2, a["w"], a["wg"], a["b"], None, None, d, a["out"], ws, stream=0) == INVALID
     assert m.k3moe_layer_routed(x, 2, i.long(), w, A16, None, None, None, m.make_dims(64, 64, 4, 4, 0), x, ws,
                                 stream=0) == INVALID
+
+
+def test_binding_rejects_host_tensors(m):
+    """Right in type and layout, but not in the device's memory."""
+    import torch
+    bf = torch.bfloat16
+    i, w = torch.empty(2, 4, dtype=torch.int32), torch.empty(2, 4)
+    assert m.k3moe_gate(torch.empty(2, 64), 2, None, m.make_gate(64, 4), i, w, 0) == INVALID
+    ws = torch.zeros(1 << 20, dtype=torch.uint8)
+    x = torch.empty(2, 64, dtype=bf)
+    assert m.k3moe_linear(x, 2, torch.empty(64, 64, dtype=bf), None, None, None, None, m.make_linear(64, 64), x.clone(), ws,
+                          stream=0) == INVALID
+    assert m.k3moe_layer_routed(x, 2, i, w, A16, None, None, None, m.make_dims(64, 64, 4, 4, 0), x, ws,
+                                stream=0) == INVALID
+
+
+def test_binding_argument_errors(m):
+    """What is not an address, a descriptor or a number raises; addresses go
+    to the library, which refuses these before any launch."""
+    g, d = m.make_gate(64, 4), m.make_linear(64, 64)
+    for bad in (("x", 1, None, g, A16, A16, 0), (A16, "1", None, g, A16, A16, 0), (A16, 1, None, d, A16, A16, 0),
+                (A16, 1, None, 5, A16, A16, 0), (A16, 1, None, g, 1.5, A16, 0), (A16, 1, None, g, A16, A16, "s")):
+        with pytest.raises((TypeError, AttributeError)):
+            m.k3moe_gate(*bad)
+    with pytest.raises(OverflowError):
+        m.k3moe_gate(A16, 1 << 31, None, g, A16, A16, 0)
+    with pytest.raises(TypeError):  # a workspace given as an address needs its size
+        m.k3moe_linear(A16, 1, A16, None, None, None, None, d, A16, A16 * 16, stream=0)
+    assert m.k3moe_linear(A16, 0, A16, None, None, None, None, d, 2 * A16, A16 * 16, BIG, 0) == INVALID
+    assert m.k3moe_linear(A16, 1, A16, None, None, None, None, d, 2 * A16, A16 * 16, 16, 0) == WORKSPACE
+    assert m.k3moe_gate(A16 + 2, 1, None, g, A16, A16, 0) == INVALID
+
+    class Stream:
+        cuda_stream = 0
+    assert m.k3moe_gate(A16, 0, None, g, A16, A16, Stream()) == INVALID
 
 
 def test_layer_routed_rejects_bad_arguments(m):
