@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) pf_expert_kernel(const __grid_c
                 maps = em + (GU ? 0 : 256);
                 scmaps = em + (GU ? 384 : 640);
             }
-            if (lane == 0 && (shared || ok)) {
+            if ((shared || ok) && umma::elect()) {  // the lane that issues the copies
                 umma::tmap_acquire(maps);
                 if (GU) umma::tmap_acquire(maps + 128);
                 if (sf_dma) {

@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kUThreads, 1) umma_expert_kernel(const __grid_
                 hdr->disp_cnt = 0u;
             }
         }
-        if (!(warp == 8 && lane == 0)) pdl_wait();
+        if (warp != 8) pdl_wait();
     } else {
         pdl_trigger();
         if (warp == 10) {
@@ -449,13 +449,13 @@ __global__ void __launch_bounds__(kUThreads, 1) umma_expert_kernel(const __grid_
     auto rng = [&](int ri) { return ri == 0 ? rng0 : rng1; };
     // gate/up, before the routed range: wait for the routing (lane 0 of the
     // calling warp waits, the warp follows), then size the routed range
-    auto routed_range = [&](bool warp_wide) {
+    auto routed_range = [&] {
         int ok = 1;
         if (lane == 0) {
             ok = (!*s_abort && mbar_wait_bounded(mready, 0u, hdr, p.wait_ns)) ? 1 : 0;
             if (!ok) *s_abort = 1;
         }
-        if (warp_wide) ok = __shfl_sync(0xffffffffu, ok, 0);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) return false;
         U = *s_U;
         rng1 = make_range(S, U * nrb * nkt, G);
@@ -547,53 +547,60 @@ __global__ void __launch_bounds__(kUThreads, 1) umma_expert_kernel(const __grid_
 
     if (warp == 8) {
         // ------------------------------------------------ TMA producer --
-        if (lane == 0) {
-            int last_u = -2;
-            uint32_t ph = 0u;  // phase of the current pass over the stages
-            int it = 0, s = 0;
-            if (GU && rng0.a < rng0.b && p.route_ctas > 0) {
-                // the shared units read x as bf16 and the shared tensor maps,
-                // which the router kernel's CTAs publish by counting prep_done
-                if (!spin_geq(&hdr->prep_done, (uint32_t)p.route_ctas, p.wait_ns)) {
-                    set_status(hdr, kStTimeout);
-                    *s_abort = 1;
-                }
-                asm volatile("fence.proxy.async.global;" ::: "memory");  // before the bulk copies read x
+        // Warp-uniform loops, one elected lane issues (as the MMA warp): with
+        // all of it in one lane's branch a unit took 1500 cycles, and the
+        // weight stream waited for the issue.
+        int last_u = -2;
+        uint32_t ph = 0u;  // phase of the current pass over the stages
+        int it = 0, s = 0;
+        if (GU && rng0.a < rng0.b && p.route_ctas > 0) {
+            // the shared units read x as bf16 and the shared tensor maps,
+            // which the router kernel's CTAs publish by counting prep_done
+            if (!__all_sync(0xffffffffu, spin_geq(&hdr->prep_done, (uint32_t)p.route_ctas, p.wait_ns))) {
+                set_status(hdr, kStTimeout);
+                *s_abort = 1;
             }
-            // The B operand (and its scale words) of a unit: activation pieces
-            // written by the previous kernel of the layer.
-            auto b_src = [&](const Unit &x, const uint8_t *&bsrc, const uint8_t *&sfbsrc) {
-                if (x.shared) {
-                    bsrc = (GU ? p.ws + L.xbf : p.ws + L.hsb) + (size_t)x.kt * N * 128;
-                    sfbsrc = nullptr;
-                } else {
-                    bsrc = GU ? p.ws + L.xb + (size_t)x.kt * N * 128
-                              : p.ws + L.hb + ((size_t)x.u * nkt + x.kt) * N * 128;
-                    sfbsrc = GU ? p.ws + L.xsf + (size_t)x.kt * 2 * kSfRow * 4
-                                : p.ws + L.hsf + ((size_t)x.u * nkt + x.kt) * 2 * kSfRow * 4;
-                }
-            };
-            auto sf_dma_of = [&](const Unit &x) {
-                return p.sf_tma && !x.shared && ublob[x.u] != nullptr;
-            };
-            // B copies of stage s (after the A copies and the stage's expect_tx)
-            auto issue_b = [&](const Unit &x, int s) {
-                uint8_t *st = smem + s * SB;
-                const uint8_t *bsrc, *sfbsrc;
-                b_src(x, bsrc, sfbsrc);
-                if (sf_dma_of(x)) bulk_g2s(st + umma_sfb_off(GU, N), sfbsrc, (uint32_t)(2 * kSfRow * 4), &full[s]);
-                bulk_g2s(st + NMAT * kAtile, bsrc, (uint32_t)(N * 128), &full[s]);
-            };
-            // down: the first two stages' weight copies go out before the wait
-            // for the gate/up pass (weights need nothing from it), their B copies
-            // after (more stages in flight there slow that pass's last writes)
-            const int npre = GU ? 0 : min(min(nst, 2), rng0.b - rng0.a);
-            for (int ri = 0; ri < 2 && !*s_abort; ++ri) {
-            if (ri == 1 && (!GU || !routed_range(false))) break;
+            asm volatile("fence.proxy.async.global;" ::: "memory");  // before the bulk copies read x
+        }
+        // The B operand (and its scale words) of a unit: activation pieces
+        // written by the previous kernel of the layer.
+        auto b_src = [&](const Unit &x, const uint8_t *&bsrc, const uint8_t *&sfbsrc) {
+            if (x.shared) {
+                bsrc = (GU ? p.ws + L.xbf : p.ws + L.hsb) + (size_t)x.kt * N * 128;
+                sfbsrc = nullptr;
+            } else {
+                bsrc = GU ? p.ws + L.xb + (size_t)x.kt * N * 128
+                          : p.ws + L.hb + ((size_t)x.u * nkt + x.kt) * N * 128;
+                sfbsrc = GU ? p.ws + L.xsf + (size_t)x.kt * 2 * kSfRow * 4
+                            : p.ws + L.hsf + ((size_t)x.u * nkt + x.kt) * 2 * kSfRow * 4;
+            }
+        };
+        auto sf_dma_of = [&](const Unit &x) {
+            return p.sf_tma && !x.shared && ublob[x.u] != nullptr;
+        };
+        // B copies of stage s (after the A copies and the stage's expect_tx);
+        // the elected lane only
+        auto issue_b = [&](const Unit &x, int s) {
+            uint8_t *st = smem + s * SB;
+            const uint8_t *bsrc, *sfbsrc;
+            b_src(x, bsrc, sfbsrc);
+            if (sf_dma_of(x)) bulk_g2s(st + umma_sfb_off(GU, N), sfbsrc, (uint32_t)(2 * kSfRow * 4), &full[s]);
+            bulk_g2s(st + NMAT * kAtile, bsrc, (uint32_t)(N * 128), &full[s]);
+        };
+        // down: the first two stages' weight copies go out before the wait
+        // for the gate/up pass (weights need nothing from it), their B copies
+        // after (more stages in flight there slow that pass's last writes)
+        const int npre = GU ? 0 : min(min(nst, 2), rng0.b - rng0.a);
+        bool go = !__any_sync(0xffffffffu, *s_abort != 0);
+        for (int ri = 0; ri < 2 && go; ++ri) {
+            if (ri == 1 && (!GU || !routed_range())) break;
             const Range rg = rng(ri);
             Unit x = rg.a < rg.b ? decode(rg.a) : Unit{};
-            for (int unit = rg.a; unit < rg.b && !*s_abort; x = advance(x, ++unit, rg.b), ++it) {
-                if (it >= nst && !wait(&empty[s], ph ^ 1u)) break;
+            for (int unit = rg.a; unit < rg.b; x = advance(x, ++unit, rg.b), ++it) {
+                if (it >= nst && !mbar_wait_warp(&empty[s], ph ^ 1u, hdr, p.wait_ns, s_abort)) {
+                    go = false;
+                    break;
+                }
                 uint8_t *st = smem + s * SB;
                 const uint8_t *blob = x.shared ? nullptr : ublob[x.u];
                 const uint8_t *maps = nullptr;
@@ -612,57 +619,62 @@ __global__ void __launch_bounds__(kUThreads, 1) umma_expert_kernel(const __grid_
                     scmaps = em + (GU ? 384 : 896);
                 }
                 const bool sf_dma = sf_dma_of(x);
-                if (x.shared || blob != nullptr) {
-                    if (x.u != last_u) {
-                        if (ws_map) umma::tmap_acquire(maps);
-                        if (GU) umma::tmap_acquire(maps + 128);
-                        if (sf_dma) {
-                            umma::tmap_acquire(scmaps);
-                            if (GU) umma::tmap_acquire(scmaps + 128);
+                if (umma::elect()) {
+                    if (x.shared || blob != nullptr) {
+                        if (x.u != last_u) {
+                            if (ws_map) umma::tmap_acquire(maps);
+                            if (GU) umma::tmap_acquire(maps + 128);
+                            if (sf_dma) {
+                                umma::tmap_acquire(scmaps);
+                                if (GU) umma::tmap_acquire(scmaps + 128);
+                            }
                         }
-                        last_u = x.u;
+                        mbar_arrive_expect_tx(&full[s], (uint32_t)(NMAT * kAtile + N * 128 +
+                                                                   (sf_dma ? NMAT * 2048 + 2 * kSfRow * 4 : 0)));
+                        umma::tma_load_2d(st, maps, x.kt * 128, x.rb * RB, &full[s]);
+                        if (GU) umma::tma_load_2d(st + kAtile, maps + 128, x.kt * 128, x.rb * RB, &full[s]);
+                        if (sf_dma) {
+                            // 16 scale bytes per row: this K-tile's 8 and its neighbour's
+                            uint8_t *sfa = st + umma_sfa_off(GU, N);
+                            umma::tma_load_2d(sfa, scmaps, (x.kt >> 1) * 16, x.rb * RB, &full[s]);
+                            if (GU) umma::tma_load_2d(sfa + 2048, scmaps + 128, (x.kt >> 1) * 16, x.rb * RB, &full[s]);
+                        }
+                    } else {
+                        mbar_arrive_expect_tx(&full[s], (uint32_t)(N * 128));
                     }
-                    mbar_arrive_expect_tx(&full[s], (uint32_t)(NMAT * kAtile + N * 128 +
-                                                               (sf_dma ? NMAT * 2048 + 2 * kSfRow * 4 : 0)));
-                    umma::tma_load_2d(st, maps, x.kt * 128, x.rb * RB, &full[s]);
-                    if (GU) umma::tma_load_2d(st + kAtile, maps + 128, x.kt * 128, x.rb * RB, &full[s]);
-                    if (sf_dma) {
-                        // 16 scale bytes per row: this K-tile's 8 and its neighbour's
-                        uint8_t *sfa = st + umma_sfa_off(GU, N);
-                        umma::tma_load_2d(sfa, scmaps, (x.kt >> 1) * 16, x.rb * RB, &full[s]);
-                        if (GU) umma::tma_load_2d(sfa + 2048, scmaps + 128, (x.kt >> 1) * 16, x.rb * RB, &full[s]);
-                    }
-                } else {
-                    mbar_arrive_expect_tx(&full[s], (uint32_t)(N * 128));
+                    if (it >= npre) issue_b(x, s);
                 }
-                if (it >= npre) issue_b(x, s);
+                __syncwarp();
+                if (x.shared || blob != nullptr) last_u = x.u;
                 if (it + 1 == npre || (npre > 0 && it + 1 < npre && unit + 1 == rg.b)) {
                     // the pre-issued stages: now wait for the gate/up pass and
                     // send their B copies
                     pdl_wait();
-                    hdr->prep_done = 0u;  // every gate/up CTA has read it (that grid is complete)
-                    asm volatile("fence.proxy.async.global;" ::: "memory");  // before the bulk copies read h
-                    Unit y = decode(rg.a);
-                    for (int q = 0; q <= it; ++q, y = advance(y, rg.a + q, rg.b)) issue_b(y, q);
+                    if (umma::elect()) {
+                        hdr->prep_done = 0u;  // every gate/up CTA has read it (that grid is complete)
+                        asm volatile("fence.proxy.async.global;" ::: "memory");  // before the bulk copies read h
+                        Unit y = decode(rg.a);
+                        for (int q = 0; q <= it; ++q, y = advance(y, rg.a + q, rg.b)) issue_b(y, q);
+                    }
+                    __syncwarp();
                 }
                 if (++s == nst) {
                     s = 0;
                     ph ^= 1u;
                 }
             }
-            }
-            if (!GU && npre == 0) {
-                pdl_wait();
-                hdr->prep_done = 0u;
-            }
-            if (*s_abort) {
-                // a wait gave up somewhere: wait (bounded) for the last copy
-                // issued into each stage, so none lands after the CTA's
-                // shared memory is released
-                for (int q = 0; q < nst && q < it; ++q) {
-                    const int last = q + ((it - 1 - q) / nst) * nst;  // its last use
-                    mbar_drain(&full[q], (uint32_t)((last / nst) & 1), p.wait_ns);
-                }
+        }
+        if (!GU && npre == 0) {
+            pdl_wait();
+            if (lane == 0) hdr->prep_done = 0u;
+        }
+        if (*s_abort && lane == 0) {
+            // a wait gave up somewhere: wait (bounded) for the last copy
+            // issued into each stage, so none lands after the CTA's
+            // shared memory is released
+            for (int q = 0; q < nst && q < it; ++q) {
+                const int last = q + ((it - 1 - q) / nst) * nst;  // its last use
+                mbar_drain(&full[q], (uint32_t)((last / nst) & 1), p.wait_ns);
             }
         }
     } else if (warp >= 4 && warp < 8) {
@@ -677,7 +689,7 @@ __global__ void __launch_bounds__(kUThreads, 1) umma_expert_kernel(const __grid_
             uint32_t ph = 0u;
             int s = 0;
             for (int ri = 0; ri < 2; ++ri) {
-            if (ri == 1 && (!GU || !routed_range(true))) break;
+            if (ri == 1 && (!GU || !routed_range())) break;
             const Range rg = rng(ri);
             Unit x = rg.a < rg.b ? decode(rg.a) : Unit{};
             bool go_on = true;
@@ -798,7 +810,7 @@ __global__ void __launch_bounds__(kUThreads, 1) umma_expert_kernel(const __grid_
         bool go = true;
         int done = 0;  // stages passed in earlier ranges
         for (int ri = 0; ri < 2 && go; ++ri) {
-            if (ri == 1 && (!GU || !routed_range(true))) break;
+            if (ri == 1 && (!GU || !routed_range())) break;
             const Range rg = rng(ri);
             const int a = rg.a, n = rg.b - rg.a;
 #pragma unroll
@@ -834,7 +846,7 @@ __global__ void __launch_bounds__(kUThreads, 1) umma_expert_kernel(const __grid_
         uint32_t ph = 0u;
         bool go = true;
         for (int ri = 0; ri < 2 && go; ++ri) {
-            if (ri == 1 && (!GU || !routed_range(true))) break;
+            if (ri == 1 && (!GU || !routed_range())) break;
             const Range rg = rng(ri);
             for (int unit = rg.a; unit < rg.b && go; ++seg) {
                 Unit x = decode(unit);
@@ -910,7 +922,7 @@ __global__ void __launch_bounds__(kUThreads, 1) umma_expert_kernel(const __grid_
                          (GU ? 0 : L.umax * ceil_div(p.ff, kTileM) + ceil_div(L.ffs, kTileM));
         int seg = 0;
         for (int ri = 0; ri < 2; ++ri) {
-        if (ri == 1 && (!GU || !routed_range(true))) break;
+        if (ri == 1 && (!GU || !routed_range())) break;
         const Range rg = rng(ri);
         for (int unit = rg.a; unit < rg.b; ++seg) {
             const Unit x = decode(unit);
