@@ -812,12 +812,13 @@ k3moe_status layer_impl(const void *x, int32_t T, const float *w_router, const f
         up.resid = norm_w ? xc : nullptr;
         up.route_ctas = route_ctas;
         up.strict = (dims->flags & K3MOE_STRICT) != 0;
-        static_assert(sizeof(up.smap_d) == sizeof(smap[3]), "one tensor map");
-        memcpy(up.smap_d, smap[3], sizeof(up.smap_d));
+        static_assert(sizeof(up.smap[0]) == sizeof(smap[0]), "one tensor map");
+        memcpy(up.smap, smap, sizeof(up.smap));  // W_g, W_u
         e = launch_umma<true>(*di, up, st);
         if (e != cudaSuccess) return cuda_fail(e, "gate/up launch");
         if ((e = hk.record(st)) != cudaSuccess) return cuda_fail(e);
 
+        memcpy(up.smap[0], smap[3], sizeof(up.smap[0]));  // W_d
         e = launch_umma<false>(*di, up, st);
         if (e != cudaSuccess) return cuda_fail(e, "down launch");
         if ((e = hk.record(st)) != cudaSuccess) return cuda_fail(e);

@@ -241,10 +241,11 @@ struct UmmaParams {
     uint64_t wait_ns;  // bound of every device wait
     int strict;        // flag E8M0 NaN bytes (0xFF) among the weight scales read
     int inject;        // failure-path tests: 1 = never signal "routing loaded"
-    // down only: the shared expert's W_d tensor map (256-row boxes), encoded by
-    // the host with its real address (read from the launch parameters, so the
-    // pass can stream it before the gate/up pass completes)
-    alignas(64) uint4 smap_d[8];
+    // The shared expert's tensor maps, encoded by the host with their real
+    // addresses (read from the launch parameters, so a pass can stream them
+    // before the one ahead of it is done): gate/up: W_g and W_u; down: W_d
+    // (256-row boxes).
+    alignas(64) uint4 smap[2][8];
 };
 
 // One pipeline stage for MMA width N: the A boxes (16 KB per matrix, first,
@@ -463,7 +464,6 @@ __global__ void __launch_bounds__(kUThreads, 1) umma_expert_kernel(const __grid_
     };
     const size_t mat = (size_t)p.d * p.ff;
     const uint8_t *const *ublob = s_blob;
-    const uint8_t *smaps = p.ws + L.tmap + (size_t)L.E * kMapsPerExpert * 128;
     const int32_t *ueid = s_eid;
     const uint32_t idesc4 = umma::idesc_mxf4(N), idesc16 = umma::idesc_bf16(N);
     // TMEM columns: accumulators [buf][mat] at (buf*NMAT + mat)*64 (N <= 64), then
@@ -553,15 +553,6 @@ __global__ void __launch_bounds__(kUThreads, 1) umma_expert_kernel(const __grid_
         int last_u = -2;
         uint32_t ph = 0u;  // phase of the current pass over the stages
         int it = 0, s = 0;
-        if (GU && rng0.a < rng0.b && p.route_ctas > 0) {
-            // the shared units read x as bf16 and the shared tensor maps,
-            // which the router kernel's CTAs publish by counting prep_done
-            if (!__all_sync(0xffffffffu, spin_geq(&hdr->prep_done, (uint32_t)p.route_ctas, p.wait_ns))) {
-                set_status(hdr, kStTimeout);
-                *s_abort = 1;
-            }
-            asm volatile("fence.proxy.async.global;" ::: "memory");  // before the bulk copies read x
-        }
         // The B operand (and its scale words) of a unit: activation pieces
         // written by the previous kernel of the layer.
         auto b_src = [&](const Unit &x, const uint8_t *&bsrc, const uint8_t *&sfbsrc) {
@@ -587,11 +578,14 @@ __global__ void __launch_bounds__(kUThreads, 1) umma_expert_kernel(const __grid_
             if (sf_dma_of(x)) bulk_g2s(st + umma_sfb_off(GU, N), sfbsrc, (uint32_t)(2 * kSfRow * 4), &full[s]);
             bulk_g2s(st + NMAT * kAtile, bsrc, (uint32_t)(N * 128), &full[s]);
         };
-        // down: the first two stages' weight copies go out before the wait
-        // for the gate/up pass (weights need nothing from it), their B copies
-        // after (more stages in flight there slow that pass's last writes)
-        const int npre = GU ? 0 : min(min(nst, 2), rng0.b - rng0.a);
-        bool go = !__any_sync(0xffffffffu, *s_abort != 0);
+        // The first two stages' weight copies go out before the wait for what
+        // the previous kernel writes (weights need nothing from it), their B
+        // copies after (more stages in flight there slow that kernel's last
+        // writes).  Gate/up: the shared units' x as bf16, which the router
+        // kernel's (or the given routing's) CTAs publish by counting
+        // prep_done; down: the gate/up pass's h.
+        const int npre = min(min(nst, 2), rng0.b - rng0.a);
+        bool go = true;
         for (int ri = 0; ri < 2 && go; ++ri) {
             if (ri == 1 && (!GU || !routed_range())) break;
             const Range rg = rng(ri);
@@ -607,12 +601,8 @@ __global__ void __launch_bounds__(kUThreads, 1) umma_expert_kernel(const __grid_
                 const uint8_t *scmaps = nullptr;  // the A scale planes' maps (TMA scale path)
                 bool ws_map = true;               // the map lives in the workspace (acquire it)
                 if (x.shared) {
-                    if (GU) {
-                        maps = smaps;
-                    } else {
-                        maps = reinterpret_cast<const uint8_t *>(p.smap_d);
-                        ws_map = false;
-                    }
+                    maps = reinterpret_cast<const uint8_t *>(p.smap);
+                    ws_map = false;
                 } else {
                     const uint8_t *em = p.ws + L.tmap + (size_t)ueid[x.u] * kMapsPerExpert * 128;
                     maps = em + (GU ? 0 : 768);
@@ -623,7 +613,7 @@ __global__ void __launch_bounds__(kUThreads, 1) umma_expert_kernel(const __grid_
                     if (x.shared || blob != nullptr) {
                         if (x.u != last_u) {
                             if (ws_map) umma::tmap_acquire(maps);
-                            if (GU) umma::tmap_acquire(maps + 128);
+                            if (GU && ws_map) umma::tmap_acquire(maps + 128);
                             if (sf_dma) {
                                 umma::tmap_acquire(scmaps);
                                 if (GU) umma::tmap_acquire(scmaps + 128);
@@ -647,12 +637,19 @@ __global__ void __launch_bounds__(kUThreads, 1) umma_expert_kernel(const __grid_
                 __syncwarp();
                 if (x.shared || blob != nullptr) last_u = x.u;
                 if (it + 1 == npre || (npre > 0 && it + 1 < npre && unit + 1 == rg.b)) {
-                    // the pre-issued stages: now wait for the gate/up pass and
-                    // send their B copies
-                    pdl_wait();
+                    // the pre-issued stages: now wait, and send their B copies
+                    if constexpr (GU) {
+                        if (p.route_ctas > 0 &&
+                            !__all_sync(0xffffffffu, spin_geq(&hdr->prep_done, (uint32_t)p.route_ctas, p.wait_ns))) {
+                            set_status(hdr, kStTimeout);
+                            *s_abort = 1;
+                        }
+                    } else {
+                        pdl_wait();
+                    }
                     if (umma::elect()) {
-                        hdr->prep_done = 0u;  // every gate/up CTA has read it (that grid is complete)
-                        asm volatile("fence.proxy.async.global;" ::: "memory");  // before the bulk copies read h
+                        if (!GU) hdr->prep_done = 0u;  // every gate/up CTA has read it (that grid is complete)
+                        asm volatile("fence.proxy.async.global;" ::: "memory");  // before the bulk copies read x or h
                         Unit y = decode(rg.a);
                         for (int q = 0; q <= it; ++q, y = advance(y, rg.a + q, rg.b)) issue_b(y, q);
                     }
