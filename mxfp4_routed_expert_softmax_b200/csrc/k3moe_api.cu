@@ -536,7 +536,12 @@ k3moe_status prefill_impl(DeviceInfo &di, RouteParams rp, const k3moe_dims *dims
         pp.ngs = ffs > 0 ? ceil_div(Tq, kGroup) : 0;
         pp.ff = dims->ff;
         pp.ffs = ffs;
-        if (given) {
+        const bool small = given && Tq <= kPfGivenSmallT;  // routing, sort and item lists in one launch
+        if (small) {
+            const PfGivenSmallParams gp{pp, given->idx + (size_t)t0 * k, given->weight + (size_t)t0 * k};
+            e = launch(pf_given_small_kernel, dim3(1), dim3(kPfGivenSmallThreads), 0, st, true, gp);
+            if (e != cudaSuccess) return cuda_fail(e, "given routing launch");
+        } else if (given) {
             const PfGivenParams gp{given->idx + (size_t)t0 * k,
                                    given->weight + (size_t)t0 * k,
                                    Tq, E, k,
@@ -561,10 +566,13 @@ k3moe_status prefill_impl(DeviceInfo &di, RouteParams rp, const k3moe_dims *dims
         }
         if (routing_only) continue;
         const int nhb = ceil_div(Tq, kPfHistTok);
-        e = launch(pf_hist_kernel, dim3(nhb), dim3(kRouteThreads), 0, st, true, pp);
-        if (e == cudaSuccess) e = launch(pf_scan_kernel, dim3(1), dim3(kPfScanThreads), 0, st, true, pp);
-        if (e == cudaSuccess) e = launch(pf_place_kernel, dim3(nhb), dim3(kRouteThreads), 0, st, true, pp);
-        if (e == cudaSuccess) e = launch(pf_items_kernel, dim3(2 * di.sms), dim3(256), 0, st, true, pp);
+        e = cudaSuccess;
+        if (!small) {
+            e = launch(pf_hist_kernel, dim3(nhb), dim3(kRouteThreads), 0, st, true, pp);
+            if (e == cudaSuccess) e = launch(pf_scan_kernel, dim3(1), dim3(kPfScanThreads), 0, st, true, pp);
+            if (e == cudaSuccess) e = launch(pf_place_kernel, dim3(nhb), dim3(kRouteThreads), 0, st, true, pp);
+            if (e == cudaSuccess) e = launch(pf_items_kernel, dim3(2 * di.sms), dim3(256), 0, st, true, pp);
+        }
         if (e == cudaSuccess) e = launch(pf_prep_kernel, dim3(2 * di.sms), dim3(kRouteThreads), 0, st, true, pp);
         if (e != cudaSuccess) return cuda_fail(e, "prefill dispatch launch");
         PfUmmaParams up{};

@@ -283,23 +283,19 @@ __global__ void __launch_bounds__(kRouteThreads) pf_place_kernel(const __grid_co
 // Items of the expert kernels in run order: group by group (an expert's
 // groups are consecutive), its 128-row blocks innermost; the shared expert's
 // groups last.  Entry: (group | row block << 20, expert or -1, first position
-// or token, tokens | blob ok << 8).  One thread per (group, row block).
-__global__ void pf_items_kernel(const __grid_constant__ PfRouteParams p) {
-    pdl_wait();
-    pdl_trigger();
-    const uint8_t *ws = p.r.ws;
-    const int NG = (int)*reinterpret_cast<const volatile uint32_t *>(
-        &reinterpret_cast<const WsHeader *>(ws + p.r.L.hdr)->n_unique);
-    const int4 *grp = reinterpret_cast<const int4 *>(ws + p.P.grp);
+// or token, tokens | blob ok << 8).  One thread per (group, row block): the
+// caller's threads i0, i0 + step, ....
+__device__ __forceinline__ void pf_write_items(const PfRouteParams &p, const int4 *grp, int NG, long long i0, long long step) {
     int4 *itg = reinterpret_cast<int4 *>(p.r.ws + p.P.itg);
     int4 *itd = reinterpret_cast<int4 *>(p.r.ws + p.P.itd);
     const int nrb_ff = ceil_div(p.ff, kTileM), nrb_d = ceil_div(p.r.d, kTileM);
     const int nrbs_ff = p.ngs > 0 ? ceil_div(p.ffs, kTileM) : 0;
-    const int per = nrb_ff > nrb_d ? nrb_ff : nrb_d;
+    int per = nrb_ff > nrb_d ? nrb_ff : nrb_d;
+    if (nrbs_ff > per) per = nrbs_ff;
     const long long n = (long long)(NG + p.ngs) * per;
-    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (long long)gridDim.x * blockDim.x) {
+    for (long long i = i0; i < n; i += step) {
         const int g = (int)(i / per), rb = (int)(i - (long long)g * per);
-        const int4 gr = __ldcg(grp + g);  // (expert or -1, first position / token, tokens, blob ok)
+        const int4 gr = grp[g];  // (expert or -1, first position / token, tokens, blob ok)
         const int4 rec = make_int4(g | (rb << 20), gr.x, gr.y, gr.z | (gr.w << 8));
         if (g < NG) {
             if (rb < nrb_ff) itg[(size_t)g * nrb_ff + rb] = rec;
@@ -310,6 +306,16 @@ __global__ void pf_items_kernel(const __grid_constant__ PfRouteParams p) {
             if (rb < nrb_d) itd[(size_t)NG * nrb_d + (size_t)s * nrb_d + rb] = rec;
         }
     }
+}
+
+__global__ void pf_items_kernel(const __grid_constant__ PfRouteParams p) {
+    pdl_wait();
+    pdl_trigger();
+    const uint8_t *ws = p.r.ws;
+    const int NG = (int)*reinterpret_cast<const volatile uint32_t *>(
+        &reinterpret_cast<const WsHeader *>(ws + p.r.L.hdr)->n_unique);
+    pf_write_items(p, reinterpret_cast<const int4 *>(ws + p.P.grp), NG, (long long)blockIdx.x * blockDim.x + threadIdx.x,
+                   (long long)gridDim.x * blockDim.x);
 }
 
 // -------------------------------------------------------------- x pieces --

@@ -94,6 +94,38 @@ def test_scale_rows_of_every_alignment(orc, cfg, T):
     assert err.max() <= G1_TOL, err
 
 
+@pytest.mark.parametrize("T", [1, 8, 9, 40, 100])
+def test_wide_shared_expert(orc, T):
+    """A shared expert with more rows than the hidden size and the routed
+    experts have, so with more row blocks than any of theirs."""
+    cfg = k3gen.Config("wide_shared", d=256, ff=64, E=32, k=4, ff_shared=1536, T=0)
+    W = kdev.weights(cfg)
+    inp = kdev.DeviceInputs(cfg, T=T)
+    idx, w = random_routing(cfg, T, T + 2, 0.1)
+    y = routed(cfg, W, inp.x, idx, w, m.K3MOE_OUT_FP32).cpu().numpy()
+    tokens = sample_tokens(T, 12)
+    assert g1_error(y[tokens], oracle_y(orc, cfg, W, inp.x_host, idx, w, tokens)).max() <= G1_TOL
+    yl, il, wl = run_layer(cfg, W, inp.x, None, T)
+    got = routed(cfg, W, inp.x, il, wl)
+    assert np.array_equal(got.view(torch.int16).cpu().numpy(), yl)
+
+
+@pytest.mark.parametrize("T", [9, 33, 63, 64, 65])
+def test_sort_in_one_launch_and_in_five(orc, T):
+    """Both sides of the number of tokens up to which one CTA sorts, with all
+    tokens on one expert, with 32 picks a token and with picks left out."""
+    cfg = k3gen.Config("many", d=128, ff=64, E=200, k=32, ff_shared=64, T=0)
+    W = kdev.weights(cfg)
+    inp = kdev.DeviceInputs(cfg, T=T)
+    idx, w = random_routing(cfg, T, T, 0.2)
+    idx[:, 0] = 7
+    idx[:, 1:] = np.where(idx[:, 1:] == 7, -1, idx[:, 1:])
+    idx[3] = -1
+    y = routed(cfg, W, inp.x, idx, w, m.K3MOE_OUT_FP32).cpu().numpy()
+    tokens = sample_tokens(T, 16)
+    assert g1_error(y[tokens], oracle_y(orc, cfg, W, inp.x_host, idx, w, tokens)).max() <= G1_TOL
+
+
 @pytest.mark.parametrize("cfg,T", [(TINY, 1), (SMALL, 8), (SMALL, 100), (k3gen.CONFIGS["k3_decode"], 1),
                                    (k3gen.CONFIGS["k3_decode"], 3)])
 def test_the_layers_own_routing_gives_the_layer(cfg, T):
