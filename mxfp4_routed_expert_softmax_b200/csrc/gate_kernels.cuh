@@ -15,6 +15,8 @@ struct GateParams {
     const float *bias;   // fp32 [E] or null
     int sigmoid, groups, kept, group_top, renorm, bf16;
     int vec;             // four logits of a row (and the bias) can be loaded at once
+    int gsize, glanes_log2;  // experts of a group; log2 of the lanes that scan one (groups << it at most 32)
+    uint32_t gmul;           // e / gsize = e gmul >> 20 for e < 1024
     float scale;
     int32_t *idx;        // [T][k]
     float *weight;       // [T][k]
@@ -150,7 +152,7 @@ __device__ __noinline__ void gate_exact(const GateParams &p, long long t, GateEx
 // compare-and-store per logit and 8.0 us, and what it takes now in the design
 // notes' table.
 constexpr int kGateWarps = 4;
-constexpr int kGateCap = 160;
+constexpr int kGateCap = 160;  // a multiple of 8
 struct alignas(16) GateWarp {
     uint64_t key[kGateCap];   // value (order-preserving bits) above the inverted id
     double exact[kGateCap];
@@ -235,8 +237,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
             for (int i = 0; i < N; ++i) lm = fmaxf(lm, o[i]);  // passes over NaN
         }
         if (!p.sigmoid) {
-            mx = lm;
-            for (int q = 16; q > 0; q >>= 1) mx = fmaxf(mx, __shfl_xor_sync(all, mx, q));
+            mx = from_order_bits(__reduce_max_sync(all, order_bits(lm)));
             // NaN and +inf logits make the sum NaN, as the formula does; the
             // exponential's error (2 units and |x| half units) is small where
             // the term is
@@ -276,7 +277,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
         }
         if (p.groups > 1) {
             // lp lanes scan a group for its one or two largest values
-            const int gs = p.E / p.groups;
+            const int gs = p.gsize, lp = 1 << p.glanes_log2;
             float amax = 0.f;
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
@@ -290,15 +291,18 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
                 *reinterpret_cast<float4 *>(val + 128 * i + 4 * lane) = make_float4(v[0], v[1], v[2], v[3]);
             }
             __syncwarp();
-            int lp = 32;
-            while (lp * p.groups > 32) lp >>= 1;
-            const int g = lane / lp;
+            const int g = lane >> p.glanes_log2;
             float x1 = ninf, x2 = ninf;
             if (g < p.groups)
-                for (int e = lane % lp; e < gs; e += lp) {
-                    const float v = val[g * gs + e];
-                    x2 = fmaxf(x2, fminf(x1, v));
-                    x1 = fmaxf(x1, v);
+                for (int e = lane & (lp - 1); e < gs; e += 4 * lp) {
+                    float v[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) v[c] = e + c * lp < gs ? val[g * gs + e + c * lp] : ninf;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        x2 = fmaxf(x2, fminf(x1, v[c]));
+                        x1 = fmaxf(x1, v[c]);
+                    }
                 }
             for (int q = 1; q < lp; q <<= 1) {
                 const float y1 = __shfl_xor_sync(all, x1, q), y2 = __shfl_xor_sync(all, x2, q);
@@ -308,26 +312,28 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
             float v = p.group_top > 1 ? (x2 > ninf ? x1 + x2 : ninf) : x1;
             v = __shfl_sync(all, v, (lane * lp) & 31);
             int r = 0;
-            for (int h = 0; h < p.groups; ++h) {
-                const float x = __shfl_sync(all, v, h);
-                r += x > v || (x == v && h < lane) ? 1 : 0;
+            for (int h0 = 0; h0 < p.groups; h0 += 8) {
+#pragma unroll
+                for (int h = 0; h < 8; ++h) {
+                    const float x = __shfl_sync(all, v, (h0 + h) & 31);
+                    r += h0 + h < p.groups && (x > v || (x == v && h0 + h < lane)) ? 1 : 0;
+                }
             }
             const bool is = lane < p.groups;
             const uint32_t keep = __ballot_sync(all, is && r < p.kept);
             if (BIAS || scores) {
                 // the last group kept and the first one dropped must differ by more than their errors
-                for (int q = 16; q > 0; q >>= 1) amax = fmaxf(amax, __shfl_xor_sync(all, amax, q));
+                amax = __uint_as_float(__reduce_max_sync(all, __float_as_uint(amax)));  // not negative: in the order of its bits
                 const float vk = __shfl_sync(all, v, __ffs(__ballot_sync(all, is && r == p.kept - 1)) - 1);
                 const float vd = __shfl_sync(all, v, __ffs(__ballot_sync(all, is && r == p.kept)) - 1);
                 const float geps = p.group_top * (fine + 0x1p-22f * amax);
                 if (vk > ninf && vd > ninf && !(vk - vd > 2.f * geps)) unsettled = true;
                 if (amax == INFINITY) unsettled = true;
             }
-            const uint32_t m = (0x100000u + gs - 1) / gs;  // e / gs = e m >> 20 for e < 1024
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const uint32_t e = 128 * (i / 4) + 4 * lane + i % 4;
-                if (!((keep >> ((e * m) >> 20 & 31)) & 1u)) o[i] = ninf;
+                if (!((keep >> ((e * p.gmul) >> 20 & 31)) & 1u)) o[i] = ninf;
             }
         }
         if (BIAS || p.groups > 1) {
@@ -377,24 +383,32 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
         pos -= cnt;
         if (C > kGateCap) unsettled = true;
         if (!unsettled) {  // alike in all lanes
-            int32_t *list = reinterpret_cast<int32_t *>(s.exact);
             while (mask) {
                 const int i = __ffs(mask) - 1;
                 mask &= mask - 1u;
-                list[pos++] = 128 * (i >> 2) + 4 * lane + (i & 3);
+                const int e = 128 * (i >> 2) + 4 * lane + (i & 3);
+                s.key[pos++] = (uint64_t)order_bits(val[e] + 0.f) << 32 | (uint32_t)~e;  // -0 ranks as 0
             }
+            if (lane < 8 && C + lane < ((C + 7) & ~7)) s.key[C + lane] = 0ull;  // up to a multiple of 8: below every key
             __syncwarp();
-            for (int c = lane; c < C; c += 32) {
-                const int e = list[c];
-                const float v = coarse ? rough(gate_logit(p, t, e)) + p.bias[e] : val[e];
-                s.key[c] = (uint64_t)order_bits(v + 0.f) << 32 | (uint32_t)~e;  // -0 ranks as 0
+            if (coarse) {
+                for (int c = lane; c < C; c += 32) {
+                    const uint32_t inv_id = (uint32_t)s.key[c];
+                    const float v = rough(gate_logit(p, t, (int)~inv_id)) + p.bias[(int)~inv_id];
+                    s.key[c] = (uint64_t)order_bits(v + 0.f) << 32 | inv_id;
+                }
+                __syncwarp();
             }
-            __syncwarp();
             for (int c = lane; c < C; c += 32) {
                 const uint64_t key = s.key[c];
                 int place = 0;
-#pragma unroll 4
-                for (int j = 0; j < C; ++j) place += s.key[j] > key ? 1 : 0;
+                for (int j = 0; j < C; j += 8) {
+#pragma unroll
+                    for (int i = 0; i < 8; i += 2) {
+                        const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(&s.key[j + i]);
+                        place += (x.x > key ? 1 : 0) + (x.y > key ? 1 : 0);
+                    }
+                }
                 if (place <= p.k) {
                     s.sorted[place] = from_order_bits((uint32_t)(key >> 32));
                     s.id[place] = (int32_t)~(uint32_t)key;

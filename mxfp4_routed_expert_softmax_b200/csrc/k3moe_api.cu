@@ -1441,6 +1441,10 @@ k3moe_status k3moe_gate(const void *logits, int64_t ld, int32_t T, const float *
     p.sigmoid = gate->score == K3MOE_SCORE_SIGMOID;
     p.groups = gate->groups_kept == gate->n_groups ? 1 : gate->n_groups;  // every group kept: no groups
     p.kept = gate->groups_kept;
+    p.gsize = p.E / p.groups;
+    p.glanes_log2 = 5;
+    while ((p.groups << p.glanes_log2) > 32) --p.glanes_log2;
+    p.gmul = (0x100000u + (uint32_t)p.gsize - 1u) / (uint32_t)p.gsize;
     p.group_top = gate->group_top;
     p.renorm = (gate->flags & K3MOE_RENORM_TOPK) != 0;
     p.bf16 = bf16;
