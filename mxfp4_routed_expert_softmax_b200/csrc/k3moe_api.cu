@@ -1002,20 +1002,32 @@ k3moe_status linear_launch(const LinearParams &p, WsHeader *hdr, cudaStream_t st
         for (int bn = 64; bn <= 256; bn += 32) {
             const int ntt = ceil_div(p.T, bn);
             const long long items = (long long)nrb2 * ntt;
-            const double waves = (double)((items + di->pairs - 1) / di->pairs);
-            const double cost = waves * (nkt * (0.14 + 0.00094 * bn) + 1.2) + 3;
-            if (cost < best) {
-                best = cost;
-                pair = true;
-                a.bn = bn;
-                a.ntt = ntt;
-                a.nrb = nrb2;
+            // whole waves, then the rest in one or more parts each (4095 x
+            // 7168 x 1536 with a residual: 448 tiles on 74 pairs, the last 4
+            // in 32 parts)
+            auto tile = [&](int n) { return nkt * (0.14 + 0.00094 * n) + 1.2; };
+            const long long whole = items - items % di->pairs;
+            for (int parts = 1; parts <= 8 && bn % (32 * parts) == 0; parts *= 2) {
+                const long long rest = (items - whole) * parts;
+                if (parts > 1 && (whole == 0 || rest == 0)) break;
+                const double cost = (double)(whole / di->pairs) * tile(bn) +
+                                    (double)((rest + di->pairs - 1) / di->pairs) * tile(bn / parts) + 3;
+                if (cost < best) {
+                    best = cost;
+                    pair = true;
+                    a.bn = bn;
+                    a.ntt = ntt;
+                    a.nrb = nrb2;
+                    a.parts = parts;
+                    a.whole = (int)(parts > 1 ? whole : items);
+                }
             }
         }
     }
     s = tmap_bf16_rows(p.w, p.K, p.N, a.tw, p.ldw, gated ? 64 : 128);
     if (s == K3MOE_OK && gated) s = tmap_bf16_rows(p.wg, p.K, p.N, a.twg, p.ldw, 64);
     if (s == K3MOE_OK) s = tmap_bf16_rows(p.x, p.K, p.T, a.tx, p.ldx, pair ? a.bn / 2 : a.bn);
+    if (s == K3MOE_OK && pair && a.parts > 1) s = tmap_bf16_rows(p.x, p.K, p.T, a.tx_part, p.ldx, a.bn / a.parts / 2);
     if (s != K3MOE_OK) return s;
     const int room = kSmemLimit - 1024 - kLtHead;
     if (pair) {

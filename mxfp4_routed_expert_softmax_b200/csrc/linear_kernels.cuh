@@ -342,8 +342,10 @@ struct LinearTcParams {
     alignas(64) uint4 tw[8];
     alignas(64) uint4 twg[8];
     alignas(64) uint4 tx[8];
+    alignas(64) uint4 tx_part[8];  // pair kernel: boxes of the last wave's parts
     LinearParams p;
     int bn;          // tokens per tile (pair kernel: of the pair)
+    int whole, parts;  // pair kernel: tiles run whole (the first ones); parts of bn / parts tokens of each other tile
     int nst;         // pipeline stages
     int nrb, ntt;    // row blocks, token tiles
     int split;       // tile kernel: CTAs (one cluster) that share a tile's K
@@ -618,6 +620,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid
     if (warp == kLpEpi && lane == 0) {
         umma::prefetch_tmap(a.tw);
         umma::prefetch_tmap(a.tx);
+        if (a.parts > 1) umma::prefetch_tmap(a.tx_part);
     }
     if (warp == 0) umma::tmem_alloc_pair(tslot, 512u);
     umma::fence_before();
@@ -629,14 +632,20 @@ __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid
     const int nrow = GATED ? 64 : 128;  // output columns of one CTA's rows
     const int nk = ceil_div(p.K, kLtKStep);
     const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
-    const int items = a.nrb * a.ntt;
+    const int items = a.whole + (a.nrb * a.ntt - a.whole) * a.parts;
     // Tiles in bands of 8 token tiles, tokens innermost: the pairs at work at
     // one time share their weight rows and their tokens through L2.
+    // The tiles that would leave most pairs idle in the last wave are cut
+    // into parts of fewer tokens, an item each.
     auto tile_at = [&](int it, int &n0, int &t0) {
-        const int per = 8 * a.nrb, band = it / per, in = it - band * per;
+        const bool part = it >= a.whole;
+        const int tile = part ? a.whole + (it - a.whole) / a.parts : it;
+        const int per = 8 * a.nrb, band = tile / per, in = tile - band * per;
         const int w = min(8, a.ntt - band * 8);
         n0 = ((in / w) * 2 + rank) * nrow;
         t0 = (band * 8 + in % w) * bn;
+        if (part) t0 += (it - a.whole) % a.parts * (bn / a.parts);
+        return part ? bn / a.parts : bn;  // its tokens
     };
     auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait_warp(bar, parity, a.hdr, a.wait_ns, s_abort); };
     pdl_wait();
@@ -648,8 +657,8 @@ __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid
         bool ok = true;
         for (int it = pair; it < items && ok; it += pairs) {
             int n0, t0;
-            tile_at(it, n0, t0);
-            const int tx = t0 + rank * (bn / 2);
+            const int tn = tile_at(it, n0, t0), tx = t0 + rank * (tn / 2);
+            const void *xmap = it < a.whole ? a.tx : a.tx_part;
             for (int kt = 0; kt < nk; ++kt, ++i) {
                 if (!wait(&empty[s], ph)) {
                     ok = false;
@@ -658,10 +667,10 @@ __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid
                 if (umma::elect()) {
                     uint8_t *st = stages + s * SB;
                     const uint32_t bar = umma::mapa(smem_u32(&full[s]), 0u);
-                    if (rank == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)(2 * SB));
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)(2 * (kLtA + tn * 64)));
                     umma::tma_load_2d_pair(st, a.tw, kt * kLtKStep, n0, bar);
                     if (GATED) umma::tma_load_2d_pair(st + kLtA / 2, a.twg, kt * kLtKStep, n0, bar);
-                    umma::tma_load_2d_pair(st + kLtA, a.tx, kt * kLtKStep, tx, bar);
+                    umma::tma_load_2d_pair(st + kLtA, xmap, kt * kLtKStep, tx, bar);
                 }
                 __syncwarp();
                 if (++s == nst) {
@@ -679,7 +688,6 @@ __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid
     } else if (warp == kLpEpi + 1) {
         if (rank == 0) {
             const uint64_t adesc = umma::smem_desc(smem_u32(stages), 16u, 1024u, umma::kLayoutSw128);
-            const uint32_t idesc = umma::idesc_bf16_pair(bn);
             int s = 0, q = 0;
             uint32_t ph = 0u;
             bool ok = true;
@@ -687,6 +695,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid
                 const int buf = q & 1;
                 if (q >= 2 && !wait(&aempty[buf], (uint32_t)(((q >> 1) + 1) & 1))) break;
                 const uint32_t d = tbase + (uint32_t)(buf * 256);
+                const uint32_t idesc = umma::idesc_bf16_pair(it < a.whole ? bn : bn / a.parts);
                 for (int kt = 0; kt < nk; ++kt) {
                     if (!wait(&full[s], ph)) {
                         ok = false;
@@ -730,8 +739,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid
         int q = 0;
         for (int it = pair; it < items; it += pairs, ++q) {
             int n0, t0;
-            tile_at(it, n0, t0);
-            const int n = n0 + nl, buf = q & 1;
+            const int tn = tile_at(it, n0, t0), n = n0 + nl, buf = q & 1;
             const int left = n < p.N ? p.T - t0 : 0;  // tokens of this tile to store
             float b[8], bg[8];
             linear_bias(p.bias, n, p.N, b);
@@ -742,7 +750,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid
             auto fetch = [&](int f) {
 #pragma unroll
                 for (int h = 0; h < np; ++h)
-                    if (RESID && f < bn && f + tl + 8 * h < left) linear_resid(p, t0 + f + tl + 8 * h, n, res[h], false);
+                    if (RESID && f < tn && f + tl + 8 * h < left) linear_resid(p, t0 + f + tl + 8 * h, n, res[h], false);
             };
             fetch(hv * 16);
             bool got = wait(&afull[buf], (uint32_t)((q >> 1) & 1));
@@ -752,7 +760,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid
             if (!got) break;
             umma::fence_after();
             const uint32_t src = tbase + umma::lane_base(warp) + (uint32_t)(buf * 256);
-            for (int f = hv * 16; f < bn; f += 4 * kLpEpi) {
+            for (int f = hv * 16; f < tn; f += 4 * kLpEpi) {
                 uint32_t raw[16];
                 umma::ld16(src + f, raw);
                 umma::wait_ld();
