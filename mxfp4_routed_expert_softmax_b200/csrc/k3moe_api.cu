@@ -89,14 +89,23 @@ cudaError_t max_clusters(Kern kernel, int n, int threads, int *out) {
     return cudaOccupancyMaxActiveClusters(out, kernel, &cfg);
 }
 
-using LinearTileKernel = void (*)(const LinearTcParams);
-template <bool GATED>
-LinearTileKernel linear_tile_of(bool resid, bool fp32) {
-    return resid ? (fp32 ? linear_tile_kernel<GATED, true, true> : linear_tile_kernel<GATED, true, false>)
-                 : (fp32 ? linear_tile_kernel<GATED, false, true> : linear_tile_kernel<GATED, false, false>);
+// The instance of a kernel template of three truth values.
+using LinearTcKernel = void (*)(const LinearTcParams);
+LinearTcKernel linear_tile_variant(bool gated, bool resid, bool fp32) {
+    static const LinearTcKernel of[8] = {
+        linear_tile_kernel<false, false, false>, linear_tile_kernel<true, false, false>,
+        linear_tile_kernel<false, true, false>,  linear_tile_kernel<true, true, false>,
+        linear_tile_kernel<false, false, true>,  linear_tile_kernel<true, false, true>,
+        linear_tile_kernel<false, true, true>,   linear_tile_kernel<true, true, true>};
+    return of[(gated ? 1 : 0) + (resid ? 2 : 0) + (fp32 ? 4 : 0)];
 }
-LinearTileKernel linear_tile_variant(bool gated, bool resid, bool fp32) {
-    return gated ? linear_tile_of<true>(resid, fp32) : linear_tile_of<false>(resid, fp32);
+LinearTcKernel linear_pair_variant(bool gated, bool resid, bool vec) {
+    static const LinearTcKernel of[8] = {
+        linear_pair_kernel<false, false, false>, linear_pair_kernel<true, false, false>,
+        linear_pair_kernel<false, true, false>,  linear_pair_kernel<true, true, false>,
+        linear_pair_kernel<false, false, true>,  linear_pair_kernel<true, false, true>,
+        linear_pair_kernel<false, true, true>,   linear_pair_kernel<true, true, true>};
+    return of[(gated ? 1 : 0) + (resid ? 2 : 0) + (vec ? 4 : 0)];
 }
 
 // One-time per-device set-up: SM count and the shared-memory opt-ins.
@@ -127,13 +136,10 @@ k3moe_status device_info(DeviceInfo **out) {
         if (r == cudaSuccess) r = set_smem(linear_stream_kernel<2, true, 1>, big);
         if (r == cudaSuccess) r = set_smem(linear_stream_kernel<2, true, 2>, big);
         for (int i = 0; i < 8 && r == cudaSuccess; ++i) r = set_smem(linear_tile_variant(i & 1, i & 2, i & 4), big);
-        if (r == cudaSuccess) r = set_smem(linear_pair_kernel<false, false>, big);
-        if (r == cudaSuccess) r = set_smem(linear_pair_kernel<false, true>, big);
-        if (r == cudaSuccess) r = set_smem(linear_pair_kernel<true, false>, big);
-        if (r == cudaSuccess) r = set_smem(linear_pair_kernel<true, true>, big);
+        for (int i = 0; i < 8 && r == cudaSuccess; ++i) r = set_smem(linear_pair_variant(i & 1, i & 2, i & 4), big);
         for (int s = 2; s <= kLtMaxSplit && r == cudaSuccess; ++s)
             r = max_clusters(linear_tile_variant(true, true, false), s, kLtThreads, &di.clusters[s]);
-        if (r == cudaSuccess) r = max_clusters(linear_pair_kernel<true, true>, 2, kLpThreads, &di.pairs);
+        if (r == cudaSuccess) r = max_clusters(linear_pair_variant(true, true, true), 2, kLpThreads, &di.pairs);
         if (r != cudaSuccess) return cuda_fail(r);
         di.ready = true;
     }
@@ -1035,9 +1041,7 @@ k3moe_status linear_launch(const LinearParams &p, WsHeader *hdr, cudaStream_t st
         a.nst = std::min((room - kLpExch) / sb, kLtMaxStages);
         const int pairs = (int)std::min<long long>(di->pairs, (long long)a.nrb * a.ntt);
         const size_t bytes = 1024 + kLtHead + a.nst * sb + kLpExch;
-        auto kernel = gated ? (p.resid ? linear_pair_kernel<true, true> : linear_pair_kernel<true, false>)
-                            : (p.resid ? linear_pair_kernel<false, true> : linear_pair_kernel<false, false>);
-        e = launch_cluster(kernel, 2 * pairs, kLpThreads, bytes, 2, st, a);
+        e = launch_cluster(linear_pair_variant(gated, p.resid != nullptr, p.vec != 0), 2 * pairs, kLpThreads, bytes, 2, st, a);
         return e == cudaSuccess ? K3MOE_OK : cuda_fail(e, "linear launch");
     }
     const int sb = kLtA + a.bn * 128;

@@ -36,49 +36,60 @@ __device__ __forceinline__ void linear_act(float (&v)[NV], int act) {
     } else if (act == K3MOE_ACT_GELU_TANH) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            v[i] = 0.5f * v[i] * (1.0f + tanhf(0.79788456080286536f * (v[i] + 0.044715f * v[i] * v[i] * v[i])));
+            v[i] = __fdividef(v[i], 1.0f + __expf(-1.5957691216057308f * (v[i] + 0.044715f * v[i] * v[i] * v[i])));  // (1 + tanh u) / 2
     }
 }
 
 __device__ __forceinline__ uint16_t bf16_bits(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
 
-// The epilogues finish NV neighbouring columns of one token in a thread: one
-// access of 8 or 16 bytes to the residual and to the output (bf16, NV = 4 or
-// 8) where their rows allow it.  (One column per lane, 2-byte accesses: the down projection
-// of 4095 tokens took 114 us.)
+// A thread finishes NV outputs: element i is column n + i dn of token t + i dt.
+// Where the rows of the output and the residual are 16-byte aligned, NV
+// neighbouring columns of one token (dn = 1), in one access of 8 or 16 bytes
+// (bf16, NV = 4 or 8); elsewhere the lanes of a warp have neighbouring columns
+// and a thread walks over others.  (2-byte accesses to aligned rows: the down
+// projection of 4095 tokens took 114 us; NV neighbouring columns of unaligned
+// ones: 1245 tokens of 2553 columns 33 us.)
+struct LinearWalk {
+    int dt, dn;
+    long long tend;  // tokens up to here
+};
 template <int NV>
 struct Residual {
     uint32_t w[NV];  // fp32 bits, or NV bf16 in the first half
 };
 
-// Loads only: nothing here waits for them.
+// Loads only: nothing here waits for them.  (t, n) exists; elements that do
+// not are read as the last ones.
 template <int NV>
-__device__ __forceinline__ void linear_resid(const LinearParams &p, long long t, int n, Residual<NV> &r, bool out_fp32) {
+__device__ __forceinline__ void linear_resid(const LinearParams &p, long long t, int n, Residual<NV> &r, bool out_fp32,
+                                             const LinearWalk &k) {
     if (!p.resid) return;
+    const bool wide = p.vec && k.dn == 1 && n + NV <= p.N;
+    auto at = [&](int i) { return min(t + i * k.dt, k.tend - 1) * p.ldr + min(n + i * k.dn, p.N - 1); };
     if (out_fp32) {
-        const float *q = reinterpret_cast<const float *>(p.resid) + t * p.ldr + n;
-        if (NV % 4 == 0 && p.vec && n + NV <= p.N) {
+        const float *q = reinterpret_cast<const float *>(p.resid);
+        if (NV % 4 == 0 && wide) {
 #pragma unroll
             for (int i = 0; i < NV; i += 4) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(q + i);
+                const uint4 v = *reinterpret_cast<const uint4 *>(q + t * p.ldr + n + i);
                 r.w[i] = v.x, r.w[i + 1] = v.y, r.w[i + 2] = v.z, r.w[i + 3] = v.w;
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) r.w[i] = __float_as_uint(q[min(i, p.N - 1 - n)]);
+            for (int i = 0; i < NV; ++i) r.w[i] = __float_as_uint(q[at(i)]);
         }
     } else {
-        const uint16_t *q = reinterpret_cast<const uint16_t *>(p.resid) + t * p.ldr + n;
-        if (NV == 8 && p.vec && n + NV <= p.N) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(q);
+        const uint16_t *q = reinterpret_cast<const uint16_t *>(p.resid);
+        if (NV == 8 && wide) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(q + t * p.ldr + n);
             r.w[0] = v.x, r.w[1 % NV] = v.y, r.w[2 % NV] = v.z, r.w[3 % NV] = v.w;
-        } else if (NV == 4 && p.vec && n + NV <= p.N) {
-            const uint2 v = *reinterpret_cast<const uint2 *>(q);
+        } else if (NV == 4 && wide) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(q + t * p.ldr + n);
             r.w[0] = v.x, r.w[1 % NV] = v.y;
         } else {
             uint16_t h[NV];
 #pragma unroll
-            for (int i = 0; i < NV; ++i) h[i] = q[min(i, p.N - 1 - n)];
+            for (int i = 0; i < NV; ++i) h[i] = q[at(i)];
 #pragma unroll
             for (int i = 0; i < NV; i += 2) r.w[i / 2] = h[i] | (uint32_t)(NV > 1 ? h[(i + 1) % NV] : 0) << 16;
         }
@@ -90,7 +101,8 @@ __device__ __forceinline__ void linear_resid(const LinearParams &p, long long t,
 template <int NV>
 __device__ __forceinline__ void linear_finish(const LinearParams &p, long long t, int n, float (&v)[NV], float (&g)[NV],
                                               const float (&b)[NV], const float (&bg)[NV], const Residual<NV> &r,
-                                              bool gated, bool resid, bool out_fp32) {
+                                              bool gated, bool resid, bool out_fp32, const LinearWalk &k) {
+    const bool wide = p.vec && k.dn == 1 && n + NV <= p.N;
 #pragma unroll
     for (int i = 0; i < NV; ++i) v[i] += b[i];
     if (gated) {
@@ -113,14 +125,14 @@ __device__ __forceinline__ void linear_finish(const LinearParams &p, long long t
     }
     if (out_fp32) {
         float *q = reinterpret_cast<float *>(p.out) + t * p.ldo + n;
-        if (NV % 4 == 0 && p.vec && n + NV <= p.N) {
+        if (NV % 4 == 0 && wide) {
 #pragma unroll
             for (int i = 0; i < NV; i += 4)
                 *reinterpret_cast<float4 *>(q + i) = make_float4(v[i], v[(i + 1) % NV], v[(i + 2) % NV], v[(i + 3) % NV]);
         } else {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (n + i < p.N) q[i] = v[i];
+                if (t + i * k.dt < k.tend && n + i * k.dn < p.N) q[(long long)(i * k.dt) * p.ldo + i * k.dn] = v[i];
         }
     } else {
         uint16_t *q = reinterpret_cast<uint16_t *>(p.out) + t * p.ldo + n;
@@ -130,22 +142,22 @@ __device__ __forceinline__ void linear_finish(const LinearParams &p, long long t
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = h[2 * i % NV] | (uint32_t)h[(2 * i + 1) % NV] << 16;
-        if (NV == 8 && p.vec && n + NV <= p.N) {
+        if (NV == 8 && wide) {
             *reinterpret_cast<uint4 *>(q) = make_uint4(w[0], w[1], w[2], w[3]);
-        } else if (NV == 4 && p.vec && n + NV <= p.N) {
+        } else if (NV == 4 && wide) {
             *reinterpret_cast<uint2 *>(q) = make_uint2(w[0], w[1]);
         } else {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (n + i < p.N) q[i] = h[i];
+                if (t + i * k.dt < k.tend && n + i * k.dn < p.N) q[(long long)(i * k.dt) * p.ldo + i * k.dn] = h[i];
         }
     }
 }
 
 template <int NV>
-__device__ __forceinline__ void linear_bias(const float *bias, int n, int N, float (&b)[NV]) {
+__device__ __forceinline__ void linear_bias(const float *bias, int n, int dn, int N, float (&b)[NV]) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) b[i] = bias && n < N ? __ldg(bias + min(n + i, N - 1)) : 0.f;
+    for (int i = 0; i < NV; ++i) b[i] = bias && n < N ? __ldg(bias + min(n + i * dn, N - 1)) : 0.f;
 }
 
 // ------------------------------------------------------ few tokens: stream --
@@ -256,9 +268,9 @@ __global__ void __launch_bounds__(32 * kLsWarps) linear_stream_kernel(const __gr
         float b[1], bg[1];
         Residual<1> res;
         if (out) {
-            linear_bias(p.bias, on, p.N, b);
-            linear_bias(p.bias_g, on, p.N, bg);
-            linear_resid(p, ot, on, res, p.out_fp32);
+            linear_bias(p.bias, on, 0, p.N, b);
+            linear_bias(p.bias_g, on, 0, p.N, bg);
+            linear_resid(p, ot, on, res, p.out_fp32, LinearWalk{0, 0, T});
         }
         __syncwarp();
         float sum[NM][4] = {};
@@ -312,7 +324,7 @@ __global__ void __launch_bounds__(32 * kLsWarps) linear_stream_kernel(const __gr
                 v[0] += src[w * NM * TT * 8];
                 if (GATED) gv[0] += src[(w * NM + RG) * TT * 8];
             }
-            linear_finish(p, ot, on, v, gv, b, bg, res, GATED, p.resid != nullptr, p.out_fp32);
+            linear_finish(p, ot, on, v, gv, b, bg, res, GATED, p.resid != nullptr, p.out_fp32, LinearWalk{0, 0, T});
         }
         __syncwarp();
     }
@@ -498,13 +510,14 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
         // CTA's (a warp's lanes: one token, or two of a gated product); the
         // biases and the first residual are loaded while the MMAs run.
         constexpr int lpt = GATED ? 16 : 32, step = kLtEpi * 32 / lpt;
-        const int n = n0 + lane % lpt * 4, j0 = threadIdx.x / lpt;
+        const LinearWalk walk{0, p.vec ? 1 : lpt, p.T};
+        const int n = n0 + lane % lpt * (p.vec ? 4 : 1), j0 = threadIdx.x / lpt;
         const long long tq = (long long)t0 + rank * cpo;
         float b[4], bg[4];
         Residual<4> res;
-        linear_bias(p.bias, n, p.N, b);
-        linear_bias(p.bias_g, n, p.N, bg);
-        if (RESID && n < p.N && j0 < jmax) linear_resid(p, tq + j0, n, res, OUT32);
+        linear_bias(p.bias, n, walk.dn, p.N, b);
+        linear_bias(p.bias_g, n, walk.dn, p.N, bg);
+        if (RESID && n < p.N && j0 < jmax) linear_resid(p, tq + j0, n, res, OUT32, walk);
         __syncwarp();
         for (int c = 0; c < nch; ++c) {
             const int buf = c & 1;
@@ -548,19 +561,27 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
         if (n < p.N) {
             for (int j = j0; j < jmax; j += step) {
                 const Residual<4> r = res;
-                if (RESID && j + step < jmax) linear_resid(p, tq + j + step, n, res, OUT32);
+                if (RESID && j + step < jmax) linear_resid(p, tq + j + step, n, res, OUT32, walk);
                 float v[4] = {}, g[4] = {};
                 const float *src = red + j * 128 + (n - n0);
                 for (int s = 0; s < S; ++s, src += cpo * 128) {
                     const float *q = s == rank ? own + j * 128 : src;
-                    const float4 x = *reinterpret_cast<const float4 *>(q);
-                    v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
-                    if (GATED) {
-                        const float4 y = *reinterpret_cast<const float4 *>(q + 64);
-                        g[0] += y.x, g[1] += y.y, g[2] += y.z, g[3] += y.w;
+                    if (p.vec) {
+                        const float4 x = *reinterpret_cast<const float4 *>(q);
+                        v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+                        if (GATED) {
+                            const float4 y = *reinterpret_cast<const float4 *>(q + 64);
+                            g[0] += y.x, g[1] += y.y, g[2] += y.z, g[3] += y.w;
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            v[i] += q[i * lpt];
+                            if (GATED) g[i] += q[64 + i * lpt];
+                        }
                     }
                 }
-                linear_finish(p, tq + j, n, v, g, b, bg, r, GATED, RESID, OUT32);
+                linear_finish(p, tq + j, n, v, g, b, bg, r, GATED, RESID, OUT32, walk);
             }
         }
     }
@@ -587,7 +608,9 @@ constexpr int kLpEpi = 16;                  // epilogue warps: four per lane qua
 constexpr int kLpThreads = 32 * (kLpEpi + 2);
 constexpr int kLpExch = kLpEpi * 16 * kLpRow * 4;
 
-template <bool GATED, bool RESID>
+// VEC: p.vec (a choice at run time cost the aligned case 2 to 4 us: 1024 x 7168
+// x 1536 with a residual 24.5 us, 28.3 with it).
+template <bool GATED, bool RESID, bool VEC>
 __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid_constant__ LinearTcParams a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -733,24 +756,25 @@ __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid
         float *ex = reinterpret_cast<float *>(stages + nst * SB);
         float *mine = ex + warp * kLpRow * 16;  // [16 tokens][32 columns]
         const float *vs = ex + (GATED ? warp & ~2 : warp) * kLpRow * 16, *gs = ex + (warp | 2) * kLpRow * 16;
+        const LinearWalk walk{VEC ? 0 : 1, VEC ? 1 : 0, p.T};  // not VEC: a thread has one column of 8 tokens
         constexpr int np = GATED ? 1 : 2;                            // passes of 8 tokens
-        const int tl = (GATED ? (quad >> 1) * 8 : 0) + lane / 4; // first token of this thread in a group
-        const int nl = 32 * (GATED ? quad & 1 : quad) + (lane & 3) * 8;
+        const int tl = (GATED ? (quad >> 1) * 8 : 0) + (VEC ? lane / 4 : 0); // first token of this thread in a group
+        const int nl = 32 * (GATED ? quad & 1 : quad) + (VEC ? (lane & 3) * 8 : lane);
         int q = 0;
         for (int it = pair; it < items; it += pairs, ++q) {
             int n0, t0;
             const int tn = tile_at(it, n0, t0), n = n0 + nl, buf = q & 1;
             const int left = n < p.N ? p.T - t0 : 0;  // tokens of this tile to store
             float b[8], bg[8];
-            linear_bias(p.bias, n, p.N, b);
-            linear_bias(p.bias_g, n, p.N, bg);
+            linear_bias(p.bias, n, walk.dn, p.N, b);
+            linear_bias(p.bias_g, n, walk.dn, p.N, bg);
             // Residuals, one group ahead of their use (the first while the
             // tile's MMAs run).
             Residual<8> res[np];
             auto fetch = [&](int f) {
 #pragma unroll
                 for (int h = 0; h < np; ++h)
-                    if (RESID && f < tn && f + tl + 8 * h < left) linear_resid(p, t0 + f + tl + 8 * h, n, res[h], false);
+                    if (RESID && f < tn && f + tl + 8 * h < left) linear_resid(p, t0 + f + tl + 8 * h, n, res[h], false, walk);
             };
             fetch(hv * 16);
             bool got = wait(&afull[buf], (uint32_t)((q >> 1) & 1));
@@ -769,22 +793,32 @@ __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid
                 __syncwarp();
                 if (GATED) umma::bar_sync(1 + peer, 64);
                 float v[np][8], g[np][8];
+                if (!VEC) {
 #pragma unroll
-                for (int h = 0; h < np; ++h)
+                    for (int h = 0; h < np; ++h)
 #pragma unroll
-                    for (int e = 0; e < 8; e += 4) {
-                        const int o = (tl + 8 * h) * kLpRow + (lane & 3) * 8 + e;
-                        const float4 x = *reinterpret_cast<const float4 *>(vs + o);
-                        v[h][e] = x.x, v[h][e + 1] = x.y, v[h][e + 2] = x.z, v[h][e + 3] = x.w;
-                        if (GATED) {
-                            const float4 y = *reinterpret_cast<const float4 *>(gs + o);
-                            g[h][e] = y.x, g[h][e + 1] = y.y, g[h][e + 2] = y.z, g[h][e + 3] = y.w;
+                        for (int e = 0; e < 8; ++e) {
+                            v[h][e] = vs[(tl + 8 * h + e) * kLpRow + lane];
+                            if (GATED) g[h][e] = gs[(tl + 8 * h + e) * kLpRow + lane];
                         }
-                    }
+                } else {
+#pragma unroll
+                    for (int h = 0; h < np; ++h)
+#pragma unroll
+                        for (int e = 0; e < 8; e += 4) {
+                            const int o = (tl + 8 * h) * kLpRow + (lane & 3) * 8 + e;
+                            const float4 x = *reinterpret_cast<const float4 *>(vs + o);
+                            v[h][e] = x.x, v[h][e + 1] = x.y, v[h][e + 2] = x.z, v[h][e + 3] = x.w;
+                            if (GATED) {
+                                const float4 y = *reinterpret_cast<const float4 *>(gs + o);
+                                g[h][e] = y.x, g[h][e + 1] = y.y, g[h][e + 2] = y.z, g[h][e + 3] = y.w;
+                            }
+                        }
+                }
 #pragma unroll
                 for (int h = 0; h < np; ++h)
                     if (f + tl + 8 * h < left)
-                        linear_finish(p, (long long)t0 + f + tl + 8 * h, n, v[h], g[h], b, bg, res[h], GATED, RESID, false);
+                        linear_finish(p, (long long)t0 + f + tl + 8 * h, n, v[h], g[h], b, bg, res[h], GATED, RESID, false, walk);
                 fetch(f + 4 * kLpEpi);
                 __syncwarp();
                 if (GATED) umma::bar_sync(1 + peer, 64);
