@@ -129,8 +129,8 @@ __device__ __noinline__ void gate_exact(const GateParams &p, long long t, GateEx
     }
 }
 
-// One warp per token, its logits in registers (lane l holds ids 128 i + 4 l ..
-// + 3).  The selection is a filter with an error bound:
+// One warp per token, its logits in registers (lane l holds ids 128 i + 4 l
+// to + 3): no exchange between warps, and 4096 tokens fill the device once.  The selection is a filter with an error bound:
 //   - without a bias the ranking is the logits' own and exact; with one the
 //     values c_e are formed in 32 bits, each within eps of the true one
 //     (sigmoid scores first by the hardware's tanh, within 2^-10);
@@ -147,10 +147,12 @@ __device__ __noinline__ void gate_exact(const GateParams &p, long long t, GateEx
 // Weights are 32-bit: the scores of the picks from expf, the softmax's argument
 // l - max with its rounding error carried along.
 //
-// Bound by instruction issue (896 experts: about 20 per logit, for 4 bytes);
-// 4096 tokens x 896, softmax, top 16: 1450 instructions a token with a
-// compare-and-store per logit and 8.0 us, and what it takes now in the design
-// notes' table.
+// Bound by instruction issue: about 1000 instructions a token of 896 experts
+// (3.6 kB), so 4096 tokens, softmax, top 16, take 6.6 us where their bytes take
+// 2.3 (8.0 us with a compare and a store per logit, 45 us with a warp-wide
+// maximum per pick over 64-bit values in shared memory).  8191 tokens, sigmoid
+// with a bias: 14.8 us (4.6), of which one in some hundred tokens needs 64
+// bits.  A single token: 3.0 us, the chain of the steps above.
 constexpr int kGateWarps = 4;
 constexpr int kGateCap = 160;  // a multiple of 8
 struct alignas(16) GateWarp {

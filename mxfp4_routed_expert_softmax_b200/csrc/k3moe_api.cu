@@ -979,7 +979,7 @@ k3moe_status linear_launch(const LinearParams &p, WsHeader *hdr, cudaStream_t st
     // two: 8.1; in 120 of 112 tokens, K in five: 9.5; 50 x 2048 x 512 in 64
     // CTAs, K in two: 4.2; in 96, K in three: 5.1).
     const int nrb = ceil_div(p.N, gated ? 64 : 128);
-    const int chain = p.out_fp32 ? kLtChain : nkt;
+    const int chain = p.out_fp32 ? kLtChain : kLtChainBf16;
     double best = 1e300;
     for (int bn = 16; bn <= 256; bn += 16) {
         const int ntt = ceil_div(p.T, bn);
@@ -1003,7 +1003,7 @@ k3moe_status linear_launch(const LinearParams &p, WsHeader *hdr, cudaStream_t st
     }
     a.nrb = nrb;
     bool pair = false;
-    if (!p.out_fp32 && di->pairs > 0) {
+    if (!p.out_fp32 && nkt <= kLpMaxSteps && di->pairs > 0) {
         const int nrb2 = ceil_div(nrb, 2);
         for (int bn = 64; bn <= 256; bn += 32) {
             const int ntt = ceil_div(p.T, bn);

@@ -171,7 +171,9 @@ __device__ __forceinline__ void linear_bias(const float *bias, int n, int dn, in
 // order is used for weights and tokens, so the order of k inside a step is
 // free and two MMAs take them as they are.  (Loads straight into the operand
 // registers, 8 lines each: one token's 896 x 7168 took 4.4 us to arrive; bulk
-// copies of 512-byte rows: 4.7 us.)
+// copies of 512-byte rows: 4.7 us; this: 3.3 us.)  Bound by memory where K and n
+// are large (7168 x 7168: 19 us, 5.4 TB/s), by latency below (4 tokens, 680 x
+// 680: 2.1 us).
 constexpr int kLsMaxT = 16;
 constexpr int kLsWarps = 8;
 constexpr int kLsMaxStages = 4;
@@ -347,7 +349,9 @@ constexpr int kLtA = 128 * 128;  // bytes of the weight box per stage
 constexpr int kLtHead = 1024;    // barriers, before the stages
 constexpr int kLtMaxStages = 10;
 constexpr int kLtMaxSplit = 8;
-constexpr int kLtChain = 8;      // K-steps per accumulation chain of an fp32 output
+constexpr int kLtChain = 8;        // K-steps per accumulation chain of an fp32 output
+constexpr int kLtChainBf16 = 256;  // and of a bf16 one; the pair kernel has one chain,
+constexpr int kLpMaxSteps = 512;   // and takes K up to this many steps
 constexpr int kLinearMaxT = 1 << 30;
 
 struct LinearTcParams {
@@ -372,13 +376,15 @@ struct LinearTcParams {
 // share its K: each accumulates its part, sends every CTA of the cluster the
 // columns that CTA finishes (one bulk copy each over distributed shared
 // memory; stores of single values took 1.8 us for 112 columns), and finishes
-// its own columns, adding the parts in rank order.
+// its own columns, adding the parts in rank order.  Bound by memory and the way
+// in (64 bytes a clock per SM): gated 100 tokens x 1536 x 7168, K in five, 14.1 us
+// for 44 MB, of which the stream takes 8.8, the exchange 1.5, the ends the rest.
 //
 // The tensor core cuts its running sum at every step, so a long chain drifts:
 // with fp32 outputs the sum moves to shared memory every `chain` K-steps (two
-// tensor-memory buffers) and the pieces are added there, rounded to nearest;
-// bf16 outputs take one chain, whose drift (2^-24 a step of 16) is far below
-// the output's half step of 2^-9.
+// tensor-memory buffers) and the pieces are added there, rounded to nearest.
+// A step of 16 costs about 2^-27 of the sum (measured over 1344 steps), so a
+// bf16 output, whose half step is 2^-9, takes chains of up to 16384 columns.
 template <bool GATED, bool RESID, bool OUT32>
 __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid_constant__ LinearTcParams a) {
     extern __shared__ uint8_t smem_raw[];
@@ -602,7 +608,11 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
 // weight rows x bn tokens, each CTA of the pair loading its 128 weight rows
 // and half of the tokens, so every operand byte a pair brings in feeds twice
 // the MMA work of a single CTA's tile.  Two tensor-memory buffers: the
-// epilogue of a tile runs under the next tile's MMAs.
+// epilogue of a tile runs under the next tile's MMAs.  Bound by the tensor
+// cores under the power limit, and by whole waves of tiles: 4096 tokens x 7168 x
+// 7168 at 1.46 PFLOP/s, gated 4096 x 1536 x 7168 at 1.42, 4095 x 7168 x 1536 with
+// a residual at 1.28.  Issue loops that keep one lane in a branch (without
+// elect) ran the MMAs at two thirds of that.
 constexpr int kLpRow = 36;                  // floats from token to token of the epilogue's buffers (4 off: no bank conflicts)
 constexpr int kLpEpi = 16;                  // epilogue warps: four per lane quadrant
 constexpr int kLpThreads = 32 * (kLpEpi + 2);

@@ -117,6 +117,7 @@ def test_layer_sizes(T, n, k, gated, act, resid, fp32):
     (17, 896, 7168, False, "none", False, True), (40, 130, 20000, False, "gelu", True, True),
     (300, 64, 16384, False, "none", False, True), (100, 1536, 7168, True, "silu", False, False),
     (129, 65, 9000, True, "silu", True, True), (500, 129, 2504, False, "relu", True, False),
+    (600, 300, 40000, False, "none", True, False), (20, 3000, 70000, True, "relu", False, False),
     # CTA pairs: ragged rows, columns and K
     (1500, 3001, 520, True, "silu", True, False), (2047, 1000, 328, False, "none", False, False),
     (1111, 2500, 1000, False, "gelu", True, False), (5000, 130, 2056, True, "relu", False, False),
