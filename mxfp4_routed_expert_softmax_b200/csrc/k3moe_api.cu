@@ -956,7 +956,11 @@ k3moe_status linear_launch(const LinearParams &p, WsHeader *hdr, cudaStream_t st
     DeviceInfo *di;
     k3moe_status s = device_info(&di);
     if (s != K3MOE_OK) return s;
-    if (p.T <= kLsMaxT) {
+    const bool gated = p.wg != nullptr;
+    // 9 to 16 tokens stream up to 40 MB of weights, and tiles take more (12
+    // tokens, 22 MB: 7.7 us streamed, 8.8 in tiles; 44 MB: 13.5, 12.9; 103 MB:
+    // 26.6, 21.4); up to 8 always stream (103 MB: 18.8, 21.5).
+    if (p.T <= kLsMaxT && (p.T <= 8 || 2LL * p.N * p.K * (gated ? 2 : 1) <= 40000000)) {
         LinearStreamParams a;
         a.p = p;
         a.hdr = hdr;
@@ -968,7 +972,6 @@ k3moe_status linear_launch(const LinearParams &p, WsHeader *hdr, cudaStream_t st
     a.p = p;
     a.hdr = hdr;
     a.wait_ns = wait_limit();
-    const bool gated = p.wg != nullptr;
     const int nkt = ceil_div(p.K, kLtKStep);
     // The variant of the least estimated time, in us as measured on B200.  A
     // K-step of a tile takes what an SM takes in (64 bytes a clock) and a
@@ -987,7 +990,7 @@ k3moe_status linear_launch(const LinearParams &p, WsHeader *hdr, cudaStream_t st
         const long long units = (long long)nrb * ntt;
         for (int c = 1; c <= kLtMaxSplit && 2 * c <= std::max(nkt, 2); ++c) {
             const int steps = ceil_div(nkt, c);
-            if (bn > 128 && (c > 1 || steps > chain)) break;
+            if (bn > 128 && c > 1) break;  // no room for both
             const int room = c > 1 ? di->clusters[c] : di->sms;  // clusters at a time
             if (room < 1) continue;
             const double waves = (double)((units + room - 1) / room);
@@ -1047,15 +1050,12 @@ k3moe_status linear_launch(const LinearParams &p, WsHeader *hdr, cudaStream_t st
     const int sb = kLtA + a.bn * 128;
     const int steps = ceil_div(nkt, a.split);
     a.chain = std::min(chain, steps);
-    const bool chains = steps > a.chain;
-    // one chain: a CTA's own sums lie over its finished stages
-    const int red = a.split > 1 ? a.split * ceil_div(a.bn, a.split) * 512 : 0, part = a.bn * 512;
-    a.nst = std::min({(room - red - (chains ? part : 0)) / sb, kLtMaxStages, std::max(steps, 2)});
-    const int stages = std::max(a.nst * sb, chains ? 0 : part);
-    a.part = kLtHead + (chains ? stages : 0);
-    a.red = kLtHead + stages + (chains ? part : 0);
+    // a CTA's own sums lie over its finished stages, the others' behind them
+    const int red = a.split > 1 ? a.split * ceil_div(a.bn, a.split) * 512 : 0;
+    a.nst = std::min({(room - red) / sb, kLtMaxStages, std::max(steps, 2)});
+    a.red = kLtHead + std::max(a.nst * sb, a.bn * 512);
     a.tcols = 32;
-    while (a.tcols < (chains ? 2 : 1) * a.bn) a.tcols *= 2;
+    while (a.tcols < (steps > a.chain ? 2 : 1) * a.bn) a.tcols *= 2;
     const int bytes = 1024 + a.red + red;
     e = launch_cluster(linear_tile_variant(gated, p.resid != nullptr, p.out_fp32 != 0), a.nrb * a.ntt * a.split, kLtThreads,
                        bytes, a.split, st, a);

@@ -367,7 +367,7 @@ struct LinearTcParams {
     int split;       // tile kernel: CTAs (one cluster) that share a tile's K
     int chain;       // tile kernel: K-steps accumulated in tensor memory at a stretch
     int tcols;       // tensor-memory columns
-    int part, red;   // tile kernel: offsets of its own sums and of the other CTAs' parts
+    int red;         // tile kernel: offset of the other CTAs' parts
     WsHeader *hdr;
     uint64_t wait_ns;
 };
@@ -381,7 +381,7 @@ struct LinearTcParams {
 // for 44 MB, of which the stream takes 8.8, the exchange 1.5, the ends the rest.
 //
 // The tensor core cuts its running sum at every step, so a long chain drifts:
-// with fp32 outputs the sum moves to shared memory every `chain` K-steps (two
+// with fp32 outputs the sum moves to registers every `chain` K-steps (two
 // tensor-memory buffers) and the pieces are added there, rounded to nearest.
 // A step of 16 costs about 2^-27 of the sum (measured over 1344 steps), so a
 // bf16 output, whose half step is 2^-9, takes chains of up to 16384 columns.
@@ -441,9 +441,9 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
     pdl_wait();
     pdl_trigger();
 
-    // part[column][row]: this CTA's sums (of the chains so far); red[source][
+    // part[column][row]: this CTA's sums, over its finished stages; red[source][
     // column][row]: the other CTAs' parts of the columns this CTA finishes.
-    float *part = reinterpret_cast<float *>(smem + a.part);
+    float *part = reinterpret_cast<float *>(stages);
     float *red = reinterpret_cast<float *>(smem + a.red);
     const int cend = min(bn, p.T - t0);                     // columns that exist
     const int jmax = max(0, min(cpo, cend - rank * cpo));   // of them, finished here
@@ -525,23 +525,25 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
         linear_bias(p.bias_g, n, walk.dn, p.N, bg);
         if (RESID && n < p.N && j0 < jmax) linear_resid(p, tq + j0, n, res, OUT32, walk);
         __syncwarp();
+        // A warp's rows and its columns 16 (warp / 4) + 64 i + 0..15.
+        float acc[4][16];
+        const uint32_t src0 = tbase + umma::lane_base(warp);
+        bool ok = true;
         for (int c = 0; c < nch; ++c) {
             const int buf = c & 1;
-            if (!wait(&afull[buf], (uint32_t)((c >> 1) & 1))) break;
+            ok = wait(&afull[buf], (uint32_t)((c >> 1) & 1));
+            if (!ok) break;
             umma::fence_after();
-            const uint32_t src = tbase + umma::lane_base(warp) + (uint32_t)(buf * bn);
-            float *dst = part + 32 * (warp & 3) + lane;
-            for (int j = 16 * (warp >> 2); j < cend; j += 4 * kLtEpi) {
-                uint32_t r[16];
-                umma::ld16(src + j, r);
-                umma::wait_ld();
-                float *d = dst + j * 128;
-                if (c == 0) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) d[i * 128] = __uint_as_float(r[i]);
-                } else {
+            for (int i = 0; i < 4; ++i) {
+                const int j = 16 * (warp >> 2) + 64 * i;
+                if (j < cend) {
+                    uint32_t r[16];
+                    umma::ld16(src0 + (uint32_t)(buf * bn + j), r);
+                    umma::wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) d[i * 128] += __uint_as_float(r[i]);
+                    for (int q = 0; q < 16; ++q)
+                        acc[i][q] = c == 0 ? __uint_as_float(r[q]) : acc[i][q] + __uint_as_float(r[q]);
                 }
             }
             umma::fence_before();
@@ -550,6 +552,17 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
                 asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&aempty[buf])) : "memory");
             __syncwarp();
         }
+        if (ok) {  // the MMAs have read every stage: the sums may lie over them
+            float *dst = part + 32 * (warp & 3) + lane;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int j = 16 * (warp >> 2) + 64 * i;
+                if (j < cend)
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) dst[(j + q) * 128] = acc[i][q];
+            }
+        }
+        __syncwarp();
         if (S > 1) fence_proxy_async();  // the copies below read what was stored here
         umma::bar_sync(1, 32 * kLtEpi);
         if (S > 1) {

@@ -118,6 +118,12 @@ def test_layer_sizes(T, n, k, gated, act, resid, fp32):
     (300, 64, 16384, False, "none", False, True), (100, 1536, 7168, True, "silu", False, False),
     (129, 65, 9000, True, "silu", True, True), (500, 129, 2504, False, "relu", True, False),
     (600, 300, 40000, False, "none", True, False), (20, 3000, 70000, True, "relu", False, False),
+    # few tokens in tiles, for more weights than are streamed for them
+    (12, 3001, 3504, True, "silu", True, False), (16, 2600, 8200, False, "none", True, True),
+    (9, 2563, 8008, False, "gelu", False, False),
+    # fp32 outputs in tiles of up to 256 tokens, chain after chain
+    (4095, 900, 1024, False, "none", True, True), (1300, 1024, 1096, True, "silu", False, True),
+    (2500, 1001, 1240, False, "gelu", True, True), (3000, 896, 576, False, "none", False, True),
     # CTA pairs: ragged rows, columns and K
     (1500, 3001, 520, True, "silu", True, False), (2047, 1000, 328, False, "none", False, False),
     (1111, 2500, 1000, False, "gelu", True, False), (5000, 130, 2056, True, "relu", False, False),
