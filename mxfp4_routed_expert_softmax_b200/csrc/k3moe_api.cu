@@ -99,12 +99,13 @@ LinearTcKernel linear_tile_variant(bool gated, bool resid, bool fp32) {
         linear_tile_kernel<false, true, true>,   linear_tile_kernel<true, true, true>};
     return of[(gated ? 1 : 0) + (resid ? 2 : 0) + (fp32 ? 4 : 0)];
 }
+template <bool OUT32>
 LinearTcKernel linear_pair_variant(bool gated, bool resid, bool vec) {
     static const LinearTcKernel of[8] = {
-        linear_pair_kernel<false, false, false>, linear_pair_kernel<true, false, false>,
-        linear_pair_kernel<false, true, false>,  linear_pair_kernel<true, true, false>,
-        linear_pair_kernel<false, false, true>,  linear_pair_kernel<true, false, true>,
-        linear_pair_kernel<false, true, true>,   linear_pair_kernel<true, true, true>};
+        linear_pair_kernel<false, false, false, OUT32>, linear_pair_kernel<true, false, false, OUT32>,
+        linear_pair_kernel<false, true, false, OUT32>,  linear_pair_kernel<true, true, false, OUT32>,
+        linear_pair_kernel<false, false, true, OUT32>,  linear_pair_kernel<true, false, true, OUT32>,
+        linear_pair_kernel<false, true, true, OUT32>,   linear_pair_kernel<true, true, true, OUT32>};
     return of[(gated ? 1 : 0) + (resid ? 2 : 0) + (vec ? 4 : 0)];
 }
 
@@ -136,10 +137,11 @@ k3moe_status device_info(DeviceInfo **out) {
         if (r == cudaSuccess) r = set_smem(linear_stream_kernel<2, true, 1>, big);
         if (r == cudaSuccess) r = set_smem(linear_stream_kernel<2, true, 2>, big);
         for (int i = 0; i < 8 && r == cudaSuccess; ++i) r = set_smem(linear_tile_variant(i & 1, i & 2, i & 4), big);
-        for (int i = 0; i < 8 && r == cudaSuccess; ++i) r = set_smem(linear_pair_variant(i & 1, i & 2, i & 4), big);
+        for (int i = 0; i < 8 && r == cudaSuccess; ++i) r = set_smem(linear_pair_variant<false>(i & 1, i & 2, i & 4), big);
+        for (int i = 0; i < 8 && r == cudaSuccess; ++i) r = set_smem(linear_pair_variant<true>(i & 1, i & 2, i & 4), big);
         for (int s = 2; s <= kLtMaxSplit && r == cudaSuccess; ++s)
             r = max_clusters(linear_tile_variant(true, true, false), s, kLtThreads, &di.clusters[s]);
-        if (r == cudaSuccess) r = max_clusters(linear_pair_variant(true, true, true), 2, kLpThreads, &di.pairs);
+        if (r == cudaSuccess) r = max_clusters(linear_pair_variant<true>(true, true, true), 2, kLpThreads, &di.pairs);
         if (r != cudaSuccess) return cuda_fail(r);
         di.ready = true;
     }
@@ -975,7 +977,11 @@ k3moe_status linear_launch(const LinearParams &p, WsHeader *hdr, cudaStream_t st
     const int nkt = ceil_div(p.K, kLtKStep);
     // The variant of the least estimated time, in us as measured on B200.  A
     // K-step of a tile takes what an SM takes in (64 bytes a clock) and a
-    // little; of a pair, 0.14 + 0.00094 bn (bn = 96: 0.22, 256: 0.38).  Tiles:
+    // little; of a pair, 0.14 + 0.00094 bn (bn = 96: 0.22, 256: 0.38), and fp32
+    // outputs 0.03 per column, since only two chains of the next tile run
+    // under a tile's end; the same between two waves of tiles (4096 x 7168 x
+    // 1536 with a residual: 131 in pairs, 166 in tiles; 4096 x 896 x 7168, a
+    // single wave: 56, 49).  Tiles:
     // 2 at the ends, 0.02 per column for the way out, 0.3 for a split
     // reduction, 0.9 when the launch leaves less than half of the SMs free for
     // the next one's start (333 x 1001 x 1000 in 112 CTAs of 48 tokens, K in
@@ -990,12 +996,12 @@ k3moe_status linear_launch(const LinearParams &p, WsHeader *hdr, cudaStream_t st
         const long long units = (long long)nrb * ntt;
         for (int c = 1; c <= kLtMaxSplit && 2 * c <= std::max(nkt, 2); ++c) {
             const int steps = ceil_div(nkt, c);
-            if (bn > 128 && c > 1) break;  // no room for both
+            if (bn > 128 && (c > 1 || (steps > chain && !p.out_fp32))) break;  // no room for the sums
             const int room = c > 1 ? di->clusters[c] : di->sms;  // clusters at a time
             if (room < 1) continue;
             const double waves = (double)((units + room - 1) / room);
             const double step = 0.045 + (16384 + 128.0 * bn) / 121600;
-            const double cost = waves * (steps * step + 0.02 * bn) + 2 + (c > 1 ? 0.3 : 0) + (2 * units * c > di->sms ? 0.9 : 0);
+            const double cost = waves * (steps * step + 0.02 * bn) + (p.out_fp32 ? (waves - 1) * 0.03 * bn : 0) + 2 + (c > 1 ? 0.3 : 0) + (2 * units * c > di->sms ? 0.9 : 0);
             if (cost < best) {
                 best = cost;
                 a.bn = bn;
@@ -1006,7 +1012,7 @@ k3moe_status linear_launch(const LinearParams &p, WsHeader *hdr, cudaStream_t st
     }
     a.nrb = nrb;
     bool pair = false;
-    if (!p.out_fp32 && nkt <= kLpMaxSteps && di->pairs > 0) {
+    if ((p.out_fp32 || nkt <= kLpMaxSteps) && di->pairs > 0) {
         const int nrb2 = ceil_div(nrb, 2);
         for (int bn = 64; bn <= 256; bn += 32) {
             const int ntt = ceil_div(p.T, bn);
@@ -1014,7 +1020,7 @@ k3moe_status linear_launch(const LinearParams &p, WsHeader *hdr, cudaStream_t st
             // whole waves, then the rest in one or more parts each (4095 x
             // 7168 x 1536 with a residual: 448 tiles on 74 pairs, the last 4
             // in 32 parts)
-            auto tile = [&](int n) { return nkt * (0.14 + 0.00094 * n) + 1.2; };
+            auto tile = [&](int n) { return nkt * (0.14 + 0.00094 * n) + 1.2 + (p.out_fp32 ? 0.03 * n : 0); };
             const long long whole = items - items % di->pairs;
             for (int parts = 1; parts <= 8 && bn % (32 * parts) == 0; parts *= 2) {
                 const long long rest = (items - whole) * parts;
@@ -1044,16 +1050,21 @@ k3moe_status linear_launch(const LinearParams &p, WsHeader *hdr, cudaStream_t st
         a.nst = std::min((room - kLpExch) / sb, kLtMaxStages);
         const int pairs = (int)std::min<long long>(di->pairs, (long long)a.nrb * a.ntt);
         const size_t bytes = 1024 + kLtHead + a.nst * sb + kLpExch;
-        e = launch_cluster(linear_pair_variant(gated, p.resid != nullptr, p.vec != 0), 2 * pairs, kLpThreads, bytes, 2, st, a);
+        a.chain = kLtChain;
+        const auto variant = p.out_fp32 ? linear_pair_variant<true> : linear_pair_variant<false>;
+        e = launch_cluster(variant(gated, p.resid != nullptr, p.vec != 0), 2 * pairs, kLpThreads, bytes, 2, st, a);
         return e == cudaSuccess ? K3MOE_OK : cuda_fail(e, "linear launch");
     }
     const int sb = kLtA + a.bn * 128;
     const int steps = ceil_div(nkt, a.split);
     a.chain = std::min(chain, steps);
-    // a CTA's own sums lie over its finished stages, the others' behind them
-    const int red = a.split > 1 ? a.split * ceil_div(a.bn, a.split) * 512 : 0;
-    a.nst = std::min({(room - red) / sb, kLtMaxStages, std::max(steps, 2)});
-    a.red = kLtHead + std::max(a.nst * sb, a.bn * 512);
+    // a CTA's own sums lie over its finished stages, unless chains are added there
+    const bool apart = steps > a.chain && a.bn <= 128;
+    const int red = a.split > 1 ? a.split * ceil_div(a.bn, a.split) * 512 : 0, part = a.bn * 512;
+    a.nst = std::min({(room - red - (apart ? part : 0)) / sb, kLtMaxStages, std::max(steps, 2)});
+    const int stages = std::max(a.nst * sb, apart ? 0 : part);
+    a.part = kLtHead + (apart ? stages : 0);
+    a.red = kLtHead + stages + (apart ? part : 0);
     a.tcols = 32;
     while (a.tcols < (steps > a.chain ? 2 : 1) * a.bn) a.tcols *= 2;
     const int bytes = 1024 + a.red + red;

@@ -365,9 +365,9 @@ struct LinearTcParams {
     int nst;         // pipeline stages
     int nrb, ntt;    // row blocks, token tiles
     int split;       // tile kernel: CTAs (one cluster) that share a tile's K
-    int chain;       // tile kernel: K-steps accumulated in tensor memory at a stretch
+    int chain;       // K-steps accumulated in tensor memory at a stretch (pair kernel: of an fp32 output)
     int tcols;       // tensor-memory columns
-    int red;         // tile kernel: offset of the other CTAs' parts
+    int part, red;   // tile kernel: offsets of its own sums and of the other CTAs' parts
     WsHeader *hdr;
     uint64_t wait_ns;
 };
@@ -381,8 +381,9 @@ struct LinearTcParams {
 // for 44 MB, of which the stream takes 8.8, the exchange 1.5, the ends the rest.
 //
 // The tensor core cuts its running sum at every step, so a long chain drifts:
-// with fp32 outputs the sum moves to registers every `chain` K-steps (two
-// tensor-memory buffers) and the pieces are added there, rounded to nearest.
+// with fp32 outputs the sum moves to shared memory (tiles of more than 128
+// tokens: registers) every `chain` K-steps (two tensor-memory buffers) and the
+// pieces are added there, rounded to nearest.
 // A step of 16 costs about 2^-27 of the sum (measured over 1344 steps), so a
 // bf16 output, whose half step is 2^-9, takes chains of up to 16384 columns.
 template <bool GATED, bool RESID, bool OUT32>
@@ -441,9 +442,9 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
     pdl_wait();
     pdl_trigger();
 
-    // part[column][row]: this CTA's sums, over its finished stages; red[source][
+    // part[column][row]: this CTA's sums (of the chains so far); red[source][
     // column][row]: the other CTAs' parts of the columns this CTA finishes.
-    float *part = reinterpret_cast<float *>(stages);
+    float *part = reinterpret_cast<float *>(smem + a.part);
     float *red = reinterpret_cast<float *>(smem + a.red);
     const int cend = min(bn, p.T - t0);                     // columns that exist
     const int jmax = max(0, min(cpo, cend - rank * cpo));   // of them, finished here
@@ -525,44 +526,73 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
         linear_bias(p.bias_g, n, walk.dn, p.N, bg);
         if (RESID && n < p.N && j0 < jmax) linear_resid(p, tq + j0, n, res, OUT32, walk);
         __syncwarp();
-        // A warp's rows and its columns 16 (warp / 4) + 64 i + 0..15.
-        float acc[4][16];
         const uint32_t src0 = tbase + umma::lane_base(warp);
-        bool ok = true;
-        for (int c = 0; c < nch; ++c) {
-            const int buf = c & 1;
-            ok = wait(&afull[buf], (uint32_t)((c >> 1) & 1));
-            if (!ok) break;
-            umma::fence_after();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int j = 16 * (warp >> 2) + 64 * i;
-                if (j < cend) {
-                    uint32_t r[16];
-                    umma::ld16(src0 + (uint32_t)(buf * bn + j), r);
-                    umma::wait_ld();
-#pragma unroll
-                    for (int q = 0; q < 16; ++q)
-                        acc[i][q] = c == 0 ? __uint_as_float(r[q]) : acc[i][q] + __uint_as_float(r[q]);
-                }
-            }
+        float *dst = part + 32 * (warp & 3) + lane;
+        auto release = [&](int buf) {
             umma::fence_before();
             __syncwarp();
             if (lane == 0)
                 asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&aempty[buf])) : "memory");
             __syncwarp();
-        }
-        if (ok) {  // the MMAs have read every stage: the sums may lie over them
-            float *dst = part + 32 * (warp & 3) + lane;
+        };
+        if (OUT32 && bn > 128) {
+            // No room for the chains' sums in shared memory: a warp's rows and
+            // its columns 16 (warp / 4) + 64 i + 0..15 in registers, over the
+            // stages at the end.  (4096 x 896 x 7168 in 49 us, 88 in tiles of
+            // 128 tokens.  Smaller tiles in this form took 0.4 us more to
+            // fetch its code: 64 x 896 x 7168 9.0 us, 8.8.)
+            float acc[4][16];
+            bool ok = true;
+            for (int c = 0; c < nch; ++c) {
+                const int buf = c & 1;
+                ok = wait(&afull[buf], (uint32_t)((c >> 1) & 1));
+                if (!ok) break;
+                umma::fence_after();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int j = 16 * (warp >> 2) + 64 * i;
-                if (j < cend)
+                for (int i = 0; i < 4; ++i) {
+                    const int j = 16 * (warp >> 2) + 64 * i;
+                    if (j < cend) {
+                        uint32_t r[16];
+                        umma::ld16(src0 + (uint32_t)(buf * bn + j), r);
+                        umma::wait_ld();
 #pragma unroll
-                    for (int q = 0; q < 16; ++q) dst[(j + q) * 128] = acc[i][q];
+                        for (int q = 0; q < 16; ++q)
+                            acc[i][q] = c == 0 ? __uint_as_float(r[q]) : acc[i][q] + __uint_as_float(r[q]);
+                    }
+                }
+                release(buf);
+            }
+            if (ok) {  // the MMAs have read every stage: the sums may lie over them
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int j = 16 * (warp >> 2) + 64 * i;
+                    if (j < cend)
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) dst[(j + q) * 128] = acc[i][q];
+                }
+            }
+            __syncwarp();
+        } else {
+            for (int c = 0; c < nch; ++c) {
+                const int buf = c & 1;
+                if (!wait(&afull[buf], (uint32_t)((c >> 1) & 1))) break;
+                umma::fence_after();
+                for (int j = 16 * (warp >> 2); j < cend; j += 4 * kLtEpi) {
+                    uint32_t r[16];
+                    umma::ld16(src0 + (uint32_t)(buf * bn + j), r);
+                    umma::wait_ld();
+                    float *d = dst + j * 128;
+                    if (c == 0) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) d[i * 128] = __uint_as_float(r[i]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) d[i * 128] += __uint_as_float(r[i]);
+                    }
+                }
+                release(buf);
             }
         }
-        __syncwarp();
         if (S > 1) fence_proxy_async();  // the copies below read what was stored here
         umma::bar_sync(1, 32 * kLtEpi);
         if (S > 1) {
@@ -617,7 +647,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
     }
 }
 
-// Many tokens, bf16 output: persistent CTA pairs (cta_group::2), tiles of 256
+// Many tokens: persistent CTA pairs (cta_group::2), tiles of 256
 // weight rows x bn tokens, each CTA of the pair loading its 128 weight rows
 // and half of the tokens, so every operand byte a pair brings in feeds twice
 // the MMA work of a single CTA's tile.  Two tensor-memory buffers: the
@@ -625,15 +655,18 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
 // cores under the power limit, and by whole waves of tiles: 4096 tokens x 7168 x
 // 7168 at 1.46 PFLOP/s, gated 4096 x 1536 x 7168 at 1.42, 4095 x 7168 x 1536 with
 // a residual at 1.28.  Issue loops that keep one lane in a branch (without
-// elect) ran the MMAs at two thirds of that.
+// elect) ran the MMAs at two thirds of that.  fp32 outputs: the chains of the
+// tile kernel, a buffer each, added in the epilogue warps' registers; a tile's
+// end then covers two chains of the next tile, not all of it (4096 x 7168 x 1536
+// with a residual 131 us, 4096 x 7168 x 7168 360 us).
 constexpr int kLpRow = 36;                  // floats from token to token of the epilogue's buffers (4 off: no bank conflicts)
 constexpr int kLpEpi = 16;                  // epilogue warps: four per lane quadrant
 constexpr int kLpThreads = 32 * (kLpEpi + 2);
 constexpr int kLpExch = kLpEpi * 16 * kLpRow * 4;
 
-// VEC: p.vec (a choice at run time cost the aligned case 2 to 4 us: 1024 x 7168
-// x 1536 with a residual 24.5 us, 28.3 with it).
-template <bool GATED, bool RESID, bool VEC>
+// OUT32: the output's type.  VEC: p.vec (a choice at run time cost the aligned
+// case 2 to 4 us: 1024 x 7168 x 1536 with a residual 24.5 us, 28.3 with it).
+template <bool GATED, bool RESID, bool VEC, bool OUT32>
 __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid_constant__ LinearTcParams a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -677,6 +710,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid
     const uint32_t tbase = *tslot;
     const int nrow = GATED ? 64 : 128;  // output columns of one CTA's rows
     const int nk = ceil_div(p.K, kLtKStep);
+    const int chain = OUT32 ? a.chain : nk;  // K-steps per tensor-memory buffer
     const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
     const int items = a.whole + (a.nrb * a.ntt - a.whole) * a.parts;
     // Tiles in bands of 8 token tiles, tokens innermost: the pairs at work at
@@ -737,12 +771,13 @@ __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid
             int s = 0, q = 0;
             uint32_t ph = 0u;
             bool ok = true;
-            for (int it = pair; it < items && ok; it += pairs, ++q) {
-                const int buf = q & 1;
+            int it = pair, kt = 0;
+            for (; it < items && ok; ++q) {
+                const int buf = q & 1, k0 = kt, k1 = min(nk, kt + chain);
                 if (q >= 2 && !wait(&aempty[buf], (uint32_t)(((q >> 1) + 1) & 1))) break;
                 const uint32_t d = tbase + (uint32_t)(buf * 256);
                 const uint32_t idesc = umma::idesc_bf16_pair(it < a.whole ? bn : bn / a.parts);
-                for (int kt = 0; kt < nk; ++kt) {
+                for (; kt < k1; ++kt) {
                     if (!wait(&full[s], ph)) {
                         ok = false;
                         break;
@@ -751,18 +786,22 @@ __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid
                     const uint64_t ad = adesc + ((uint32_t)(s * SB) >> 4), bd = ad + (kLtA >> 4);
                     const int steps = ceil_div(p.K - kt * kLtKStep, 16);
                     if (umma::elect()) {
-                        umma::mma_bf16_pair(d, ad, bd, idesc, kt > 0 ? 1u : 0u);
+                        umma::mma_bf16_pair(d, ad, bd, idesc, kt > k0 ? 1u : 0u);
                         if (steps > 1) umma::mma_bf16_pair(d, ad + 2, bd + 2, idesc, 1u);
                         if (steps > 2) umma::mma_bf16_pair(d, ad + 4, bd + 4, idesc, 1u);
                         if (steps > 3) umma::mma_bf16_pair(d, ad + 6, bd + 6, idesc, 1u);
                         umma::commit_pair(&empty[s]);
-                        if (kt + 1 == nk) umma::commit_pair(&afull[buf]);
+                        if (kt + 1 == k1) umma::commit_pair(&afull[buf]);
                     }
                     __syncwarp();
                     if (++s == nst) {
                         s = 0;
                         ph ^= 1u;
                     }
+                }
+                if (kt == nk) {
+                    kt = 0;
+                    it += pairs;
                 }
             }
             if (umma::elect()) umma::commit_pair(mdone);
@@ -779,57 +818,113 @@ __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid
         float *ex = reinterpret_cast<float *>(stages + nst * SB);
         float *mine = ex + warp * kLpRow * 16;  // [16 tokens][32 columns]
         const float *vs = ex + (GATED ? warp & ~2 : warp) * kLpRow * 16, *gs = ex + (warp | 2) * kLpRow * 16;
-        const LinearWalk walk{VEC ? 0 : 1, VEC ? 1 : 0, p.T};  // not VEC: a thread has one column of 8 tokens
-        constexpr int np = GATED ? 1 : 2;                            // passes of 8 tokens
-        const int tl = (GATED ? (quad >> 1) * 8 : 0) + (VEC ? lane / 4 : 0); // first token of this thread in a group
-        const int nl = 32 * (GATED ? quad & 1 : quad) + (VEC ? (lane & 3) * 8 : lane);
+        // 8 bf16 or 4 fp32 outputs per thread and pass: 16 bytes (two stores of
+        // 16 bytes each, 32 apart from lane to lane, halved the rate).
+        constexpr int NV = OUT32 ? 4 : 8, LT = 32 / NV, np = (GATED ? 8 : 16) / NV;
+        const LinearWalk walk{VEC ? 0 : 1, VEC ? 1 : 0, p.T};  // not VEC: a thread has one column of NV tokens
+        const int tl = (GATED ? (quad >> 1) * 8 : 0) + (VEC ? lane / LT : 0);  // first token of this thread in a group
+        const int nl = 32 * (GATED ? quad & 1 : quad) + (VEC ? lane % LT * NV : lane);
         int q = 0;
-        for (int it = pair; it < items; it += pairs, ++q) {
+        for (int it = pair; it < items; it += pairs) {
             int n0, t0;
-            const int tn = tile_at(it, n0, t0), n = n0 + nl, buf = q & 1;
+            const int tn = tile_at(it, n0, t0), n = n0 + nl;
             const int left = n < p.N ? p.T - t0 : 0;  // tokens of this tile to store
-            float b[8], bg[8];
-            linear_bias(p.bias, n, walk.dn, p.N, b);
-            linear_bias(p.bias_g, n, walk.dn, p.N, bg);
             // Residuals, one group ahead of their use (the first while the
             // tile's MMAs run).
-            Residual<8> res[np];
+            Residual<NV> res[np];
             auto fetch = [&](int f) {
 #pragma unroll
                 for (int h = 0; h < np; ++h)
-                    if (RESID && f < tn && f + tl + 8 * h < left) linear_resid(p, t0 + f + tl + 8 * h, n, res[h], false, walk);
+                    if (RESID && f < tn && f + tl + NV * h < left) linear_resid(p, t0 + f + tl + NV * h, n, res[h], OUT32, walk);
             };
-            fetch(hv * 16);
-            bool got = wait(&afull[buf], (uint32_t)((q >> 1) & 1));
-            __syncwarp();
+            float b[NV], bg[NV];
+            auto columns = [&] {
+                linear_bias(p.bias, n, walk.dn, p.N, b);
+                linear_bias(p.bias_g, n, walk.dn, p.N, bg);
+                fetch(hv * 16);
+            };
+            float acc[OUT32 ? 4 : 1][16];  // the chains' sums of this warp's groups
+            bool got;
+            int buf = q & 1;
+            if (OUT32) {
+                for (int kt = 0; kt < nk; kt += chain, ++q) {
+                    buf = q & 1;
+                    got = wait(&afull[buf], (uint32_t)((q >> 1) & 1));
+                    __syncwarp();
+                    if (!got) break;
+                    umma::fence_after();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int f = hv * 16 + i * 4 * kLpEpi;
+                        if (f < tn) {
+#pragma unroll
+                            for (int h = 0; h < 16; h += 8) {
+                                uint32_t raw[8];
+                                umma::ld8(tbase + umma::lane_base(warp) + (uint32_t)(buf * 256 + f + h), raw);
+                                umma::wait_ld();
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) {
+                                    float &x = acc[OUT32 ? i : 0][h + j];
+                                    x = kt == 0 ? __uint_as_float(raw[j]) : x + __uint_as_float(raw[j]);
+                                }
+                            }
+                        }
+                    }
+                    umma::fence_before();
+                    __syncwarp();
+                    if (lane == 0) umma::arrive_cluster(umma::mapa(smem_u32(&aempty[buf]), 0u));
+                    __syncwarp();
+                }
+                columns();
+                __syncwarp();
+            } else {
+                columns();
+                got = wait(&afull[buf], (uint32_t)((q >> 1) & 1));
+                __syncwarp();
+            }
             // the two warps that exchange go on together or not at all
             if (GATED) got = umma::bar_red_and(1 + peer, 64, got);
             if (!got) break;
             umma::fence_after();
             const uint32_t src = tbase + umma::lane_base(warp) + (uint32_t)(buf * 256);
+#pragma unroll 1
             for (int f = hv * 16; f < tn; f += 4 * kLpEpi) {
-                uint32_t raw[16];
-                umma::ld16(src + f, raw);
-                umma::wait_ld();
+                // opaque: no loop of a lane's own around the aligned instructions
+                int lim = left;
+                asm volatile("" : "+r"(lim));
+                if (OUT32) {
+                    // the next group's sums move up: a choice among the four
+                    // would keep all of them in registers to the end
 #pragma unroll
-                for (int j = 0; j < 16; ++j) mine[j * kLpRow + lane] = __uint_as_float(raw[j]);
+                    for (int j = 0; j < 16; ++j) mine[j * kLpRow + lane] = acc[0][j];
+#pragma unroll
+                    for (int i = 0; i + 1 < (OUT32 ? 4 : 1); ++i)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) acc[i][j] = acc[i + 1][j];
+                } else {
+                    uint32_t raw[16];
+                    umma::ld16(src + f, raw);
+                    umma::wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) mine[j * kLpRow + lane] = __uint_as_float(raw[j]);
+                }
                 __syncwarp();
                 if (GATED) umma::bar_sync(1 + peer, 64);
-                float v[np][8], g[np][8];
+                float v[np][NV], g[np][NV];
                 if (!VEC) {
 #pragma unroll
                     for (int h = 0; h < np; ++h)
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            v[h][e] = vs[(tl + 8 * h + e) * kLpRow + lane];
-                            if (GATED) g[h][e] = gs[(tl + 8 * h + e) * kLpRow + lane];
+                        for (int e = 0; e < NV; ++e) {
+                            v[h][e] = vs[(tl + NV * h + e) * kLpRow + lane];
+                            if (GATED) g[h][e] = gs[(tl + NV * h + e) * kLpRow + lane];
                         }
                 } else {
 #pragma unroll
                     for (int h = 0; h < np; ++h)
 #pragma unroll
-                        for (int e = 0; e < 8; e += 4) {
-                            const int o = (tl + 8 * h) * kLpRow + (lane & 3) * 8 + e;
+                        for (int e = 0; e < NV; e += 4) {
+                            const int o = (tl + NV * h) * kLpRow + lane % LT * NV + e;
                             const float4 x = *reinterpret_cast<const float4 *>(vs + o);
                             v[h][e] = x.x, v[h][e + 1] = x.y, v[h][e + 2] = x.z, v[h][e + 3] = x.w;
                             if (GATED) {
@@ -840,15 +935,18 @@ __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid
                 }
 #pragma unroll
                 for (int h = 0; h < np; ++h)
-                    if (f + tl + 8 * h < left)
-                        linear_finish(p, (long long)t0 + f + tl + 8 * h, n, v[h], g[h], b, bg, res[h], GATED, RESID, false, walk);
+                    if (f + tl + NV * h < lim)
+                        linear_finish(p, (long long)t0 + f + tl + NV * h, n, v[h], g[h], b, bg, res[h], GATED, RESID, OUT32, walk);
                 fetch(f + 4 * kLpEpi);
                 __syncwarp();
                 if (GATED) umma::bar_sync(1 + peer, 64);
             }
-            umma::fence_before();
-            __syncwarp();
-            if (lane == 0) umma::arrive_cluster(umma::mapa(smem_u32(&aempty[buf]), 0u));
+            if (!OUT32) {
+                umma::fence_before();
+                __syncwarp();
+                if (lane == 0) umma::arrive_cluster(umma::mapa(smem_u32(&aempty[buf]), 0u));
+                ++q;
+            }
         }
     }
     __syncwarp();

@@ -127,7 +127,11 @@ def test_layer_sizes(T, n, k, gated, act, resid, fp32):
     # CTA pairs: ragged rows, columns and K
     (1500, 3001, 520, True, "silu", True, False), (2047, 1000, 328, False, "none", False, False),
     (1111, 2500, 1000, False, "gelu", True, False), (5000, 130, 2056, True, "relu", False, False),
-    (4096, 4104, 72, False, "none", True, False)])
+    (4096, 4104, 72, False, "none", True, False),
+    # CTA pairs with fp32 outputs: one chain, several, a last one of one K-step
+    (4096, 4104, 72, False, "none", True, True), (2047, 2500, 520, False, "gelu", False, True),
+    (1500, 3001, 584, True, "silu", True, True), (4095, 2304, 1096, True, "relu", False, True),
+    (3000, 7168, 1536, False, "none", True, True), (2100, 2600, 2600, False, "none", False, True)])
 def test_variants(T, n, k, gated, act, resid, fp32):
     check(data(T, n, k, T + n, gated, bias=n % 2 == 0, resid=resid, fp32=fp32), act, fp32)
 
