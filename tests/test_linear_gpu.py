@@ -285,3 +285,77 @@ def test_streams_and_graph(T, n, k):
         g.replay()
     torch.cuda.synchronize()
     assert torch.equal(oa, rb) and torch.equal(ob, rb)
+
+
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("T,n,k", [(2047, 2500, 520), (1500, 3001, 584)])
+def test_many_tokens_in_wider_rows_in_place(T, n, k, gated, fp32):
+    """Many tokens: the residual in place, in rows of a wider tensor; what lies
+    beside and behind them stays as it was, and a token or a weight row with
+    NaN touches its own row or column only."""
+    d = data(T, n, k, 4, gated, bias=True, resid=True, fp32=fp32)
+    d["x"][T - 1, 3] = float("nan")
+    d["w"][n - 1, 7] = float("nan")
+    clean = {a: None if v is None else v.clone() for a, v in d.items()}
+    clean["x"][T - 1, 3], clean["w"][n - 1, 7] = 0, 0
+    xw = torch.full((T + 2, k + 24), float("nan"), dtype=BF, device="cuda")
+    xs = xw[:T, 8:8 + k]
+    xs.copy_(d["x"])
+    for off in (0, 16, 5):
+        o = torch.full((T + 2, n + 28), 77.0, dtype=d["r"].dtype, device="cuda")
+        h = o[:T, off:off + n]
+        h.copy_(d["r"])
+        _, ws = call({**d, "x": xs, "r": h}, "silu", fp32, out=h)
+        torch.cuda.synchronize()
+        m.check(m.k3moe_device_status(ws), "device status")
+        assert torch.isnan(h[T - 1]).all() and torch.isnan(h[:, n - 1]).all()
+        ref, tol = linear_ref(clean["x"], clean["w"], clean["wg"], clean["b"], clean["bg"], clean["r"], "silu",
+                              24 if fp32 else 8)
+        ok = (h.double() - ref).abs() <= tol
+        assert ok[:T - 1, :n - 1].all()
+        o[:T, off:off + n] = 77.0
+        assert (o == 77.0).all()
+
+
+def test_fp32_precision_of_many_tokens():
+    """As above, in tiles of more tokens and in pairs of CTAs."""
+    for T, n, k in ((1300, 2560, 4096), (3000, 896, 7168)):
+        d = data(T, n, k, T)
+        out, _ = call(d, fp32=True)
+        ref = d["x"].double() @ d["w"].double().T
+        assert float((out.double() - ref).norm() / ref.norm()) <= 1e-6
+
+
+@pytest.mark.parametrize("fp32", [False, True])
+def test_many_tokens_on_two_streams(fp32):
+    """Two calls of many tokens at once, a workspace each, between calls of few
+    tokens; then captured and replayed."""
+    a, b, c = data(2047, 2500, 520, 1), data(1500, 3001, 584, 2), data(5, 896, 2048, 3)
+    want = [call(d, fp32=fp32)[0] for d in (a, b, c)]
+    torch.cuda.synchronize()
+    outs, wss = zip(*[call(d, fp32=fp32) for d in (a, b, c, c)])
+    torch.cuda.synchronize()
+    for o in outs:
+        o.zero_()
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(8):
+        call(a, fp32=fp32, out=outs[0], ws=wss[0], stream=s1)
+        call(c, fp32=fp32, out=outs[2], ws=wss[2], stream=s1)
+        call(b, fp32=fp32, out=outs[1], ws=wss[1], stream=s2)
+        call(c, fp32=fp32, out=outs[3], ws=wss[3], stream=s2)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want + [want[2]]):
+        assert torch.equal(o, w)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for d, o in zip((a, b, c), outs):
+            call(d, fp32=fp32, out=o, ws=wss[0])
+    for o in outs:
+        o.zero_()
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
