@@ -350,8 +350,8 @@ constexpr int kLtHead = 1024;    // barriers, before the stages
 constexpr int kLtMaxStages = 10;
 constexpr int kLtMaxSplit = 8;
 constexpr int kLtChain = 8;        // K-steps per accumulation chain of an fp32 output
-constexpr int kLtChainBf16 = 256;  // and of a bf16 one; the pair kernel has one chain,
-constexpr int kLpMaxSteps = 512;   // and takes K up to this many steps
+constexpr int kLtChainBf16 = 256;  // and of a bf16 one; in the pair kernel that is one chain,
+constexpr int kLpMaxSteps = 512;   // of K up to this many steps
 constexpr int kLinearMaxT = 1 << 30;
 
 struct LinearTcParams {
