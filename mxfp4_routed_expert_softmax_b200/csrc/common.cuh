@@ -143,14 +143,22 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, W
     }
 }
 
-// Wait (bounded, no status) for phase `parity` of `bar`: used on the way
-// out of a kernel whose pipeline gave up, so that bulk copies this thread
-// issued have landed before the CTA's shared memory is released.
-__device__ __forceinline__ void mbar_drain(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
-    const uint64_t t0 = globaltimer();
+// Wait (no status) for phase `parity` of `bar`, up to kWaitLimitNs after t0:
+// used on the way out of a kernel whose pipeline gave up, so that what this
+// CTA issued has ended before its memory is released.  The limit is not the
+// call's: one that was shortened would let go of copies about to land.
+__device__ __forceinline__ void mbar_drain(uint64_t *bar, uint32_t parity, uint64_t t0) {
     while (!mbar_try_wait(bar, parity)) {
-        if (globaltimer() - t0 > limit_ns) return;
+        if (globaltimer() - t0 > kWaitLimitNs) return;
     }
+}
+// The same for a ring of nst stages: the last of `issued` uses of each.  Called
+// by one thread after the CTA's closing barrier, when no role can give up any
+// more: a copying role that has issued all it had to is done before the others
+// are, and cannot know.
+__device__ __forceinline__ void drain_ring(uint64_t *full, int nst, int issued) {
+    const uint64_t t0 = globaltimer();
+    for (int s = 0; s < nst && s < issued; ++s) mbar_drain(&full[s], (uint32_t)(((issued - 1 - s) / nst) & 1), t0);
 }
 
 // E8M0 byte 0xFF encodes NaN: nonzero when any of the 8 bytes of (a, b) is.

@@ -967,6 +967,7 @@ k3moe_status linear_launch(const LinearParams &p, WsHeader *hdr, cudaStream_t st
         a.p = p;
         a.hdr = hdr;
         a.wait_ns = wait_limit();
+        a.inject = g_fault_mode.load(std::memory_order_relaxed);
         return linear_stream(*di, a, st);
     }
     cudaError_t e;
@@ -974,6 +975,7 @@ k3moe_status linear_launch(const LinearParams &p, WsHeader *hdr, cudaStream_t st
     a.p = p;
     a.hdr = hdr;
     a.wait_ns = wait_limit();
+    a.inject = g_fault_mode.load(std::memory_order_relaxed);
     const int nkt = ceil_div(p.K, kLtKStep);
     // The variant of the least estimated time, in us as measured on B200.  A
     // K-step of a tile takes what an SM takes in (64 bytes a clock) and a

@@ -792,6 +792,7 @@ __global__ void __launch_bounds__(kLThreads, 1) layer_kernel(const __grid_consta
         }
     }
 
+    int issued = 0;  // stages filled (the copying thread)
     if (warp == 8) {
         // ========================================================= copies --
         if (lane == 0) {
@@ -934,19 +935,13 @@ __global__ void __launch_bounds__(kLThreads, 1) layer_kernel(const __grid_consta
                     }
                 }
             }
-            if (npend > 0 && !*s_abort && gu_ready(true)) {
+            if (npend > 0) {
+                // after a wait that gave up too: the stages have to fill
+                if (!*s_abort) gu_ready(true);
                 for (int q = 0; q < npend; ++q) issue_b(pend_s[q], decode(3, pend_unit[q]));
                 npend = 0;
             }
-            if (*s_abort) {
-                // a wait gave up somewhere: wait (bounded) for the last copy
-                // issued into each stage, so none lands after the CTA's
-                // shared memory is released
-                for (int q = 0; q < nst && q < i; ++q) {
-                    const int last = q + ((i - 1 - q) / nst) * nst;
-                    mbar_drain(&full[q], (uint32_t)((last / nst) & 1), rp.wait_ns);
-                }
-            }
+            issued = i;
         }
     } else if (warp >= 4 && warp < 8) {
         // ============================ router sums (R0), scales -> TMEM =====
@@ -1334,7 +1329,7 @@ __global__ void __launch_bounds__(kLThreads, 1) layer_kernel(const __grid_consta
             // the CTA frees its tensor memory only after every MMA issued here
             // has completed (on an early exit too)
             umma::commit(mdone);
-            mbar_drain(mdone, 0u, rp.wait_ns);
+            mbar_drain(mdone, 0u, globaltimer());
         }
     }
 
@@ -1507,6 +1502,7 @@ __global__ void __launch_bounds__(kLThreads, 1) layer_kernel(const __grid_consta
 
     umma::fence_before();
     __syncthreads();
+    if (warp == 8 && lane == 0 && *s_abort) drain_ring(full, nst, issued);
     if (warp == 0) {
         umma::fence_after();
         umma::tmem_dealloc(tbase, kCols);

@@ -186,6 +186,7 @@ struct LinearStreamParams {
     int kc, ns;  // columns per chunk (a multiple of 64), stages per warp
     WsHeader *hdr;
     uint64_t wait_ns;
+    int inject;  // failure-path tests: the copies of one last step are never made
 };
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -236,6 +237,7 @@ __global__ void __launch_bounds__(32 * kLsWarps) linear_stream_kernel(const __gr
     int ig = warp < chunks ? blockIdx.x : groups, ic = warp, issued = 0;
     auto issue = [&](int s) {
         if (ig >= groups) return;
+        if (a.inject && warp == 0 && ic + kLsWarps >= chunks && ig + gridDim.x >= groups) return;
         if (umma::elect()) {
             uint8_t *st = ring + s * stageb;
             mbar_arrive_expect_tx(&bar[s], (uint32_t)((NM * 8 + T) * rowb));  // the other token rows stay as they are
@@ -330,10 +332,8 @@ __global__ void __launch_bounds__(32 * kLsWarps) linear_stream_kernel(const __gr
         }
         __syncwarp();
     }
-    if (*s_abort && lane == 0) {
-        // a wait gave up: wait (bounded) for this warp's copies in flight
-        for (int i = 0; i < a.ns && i < issued; ++i) mbar_drain(&bar[i], (uint32_t)(((issued - 1 - i) / a.ns) & 1), a.wait_ns);
-    }
+    // a warp that gave up waits (bounded) for its own copies in flight
+    if (!ok && lane == 0) drain_ring(bar, a.ns, issued);
 }
 
 // -------------------------------------------------------- tcgen05 kernels --
@@ -370,6 +370,7 @@ struct LinearTcParams {
     int part, red;   // tile kernel: offsets of its own sums and of the other CTAs' parts
     WsHeader *hdr;
     uint64_t wait_ns;
+    int inject;  // failure-path tests: the copies of one last step are never made
 };
 
 // A tile of 128 weight rows x bn tokens per cluster of `split` CTAs, which
@@ -449,10 +450,12 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
     const int cend = min(bn, p.T - t0);                     // columns that exist
     const int jmax = max(0, min(cpo, cend - rank * cpo));   // of them, finished here
     if (S > 1 && threadIdx.x == 0 && jmax > 0) mbar_arrive_expect_tx(rfull, (uint32_t)((S - 1) * jmax * 512));
+    int issued = 0;  // stages filled (the copying warp)
     if (warp == kLtEpi) {
         int i = 0, s = 0;
         uint32_t ph = 1u;  // of the empty barriers: the first round's waits pass at once
-        for (; i < nk; ++i) {
+        const int fill = a.inject && rank == 0 ? nk - 1 : nk;
+        for (; i < fill; ++i) {
             if (!wait(&empty[s], ph)) break;
             if (umma::elect()) {
                 uint8_t *st = stages + s * SB;
@@ -468,12 +471,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
                 ph ^= 1u;
             }
         }
-        if (*s_abort && lane == 0) {
-            for (int t = 0; t < nst && t < i; ++t) {
-                const int last = t + ((i - 1 - t) / nst) * nst;
-                mbar_drain(&full[t], (uint32_t)((last / nst) & 1), a.wait_ns);
-            }
-        }
+        issued = i;
     } else if (warp == kLtEpi + 1) {
         const uint64_t adesc = umma::smem_desc(smem_u32(stages), 16u, 1024u, umma::kLayoutSw128);
         const uint32_t idesc = umma::idesc_bf16(bn);
@@ -510,7 +508,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
         }
         if (umma::elect()) {
             umma::commit(mdone);
-            mbar_drain(mdone, 0u, a.wait_ns);
+            mbar_drain(mdone, 0u, globaltimer());
         }
     } else {
         // A thread finishes 4 columns of the tokens j0, j0 + step, ... of its
@@ -641,6 +639,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
     }
     umma::fence_before();
     __syncthreads();
+    if (warp == kLtEpi && lane == 0 && *s_abort) drain_ring(full, nst, issued);
     if (warp == 0) {
         umma::fence_after();
         umma::tmem_dealloc(tbase, (uint32_t)a.tcols);
@@ -760,10 +759,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid
             }
         }
         if (*s_abort && rank == 0 && lane == 0) {
-            for (int t = 0; t < nst && t < i; ++t) {
-                const int last = t + ((i - 1 - t) / nst) * nst;
-                mbar_drain(&full[t], (uint32_t)((last / nst) & 1), a.wait_ns);
-            }
+            drain_ring(full, nst, i);
         }
     } else if (warp == kLpEpi + 1) {
         if (rank == 0) {

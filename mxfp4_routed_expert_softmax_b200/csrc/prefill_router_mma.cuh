@@ -118,6 +118,7 @@ __global__ void __launch_bounds__(kRmThreads, 1) pf_router_mma_kernel(const __gr
         *s_abort = 1;
         return false;
     };
+    int issued = 0;  // stages filled (the copying thread)
     if (warp == 1) {
         if (lane == 0) {
             int i = 0;
@@ -133,12 +134,7 @@ __global__ void __launch_bounds__(kRmThreads, 1) pf_router_mma_kernel(const __gr
                     umma::tma_load_2d(st + 3 * kRmBox, p.tx, ks * kRmKStep, t0, &full[s]);
                 }
             }
-            if (*s_abort) {
-                for (int q = 0; q < kRmStages && q < i; ++q) {
-                    const int last = q + ((i - 1 - q) / kRmStages) * kRmStages;
-                    mbar_drain(&full[q], (uint32_t)((last / kRmStages) & 1), p.wait_ns);
-                }
-            }
+            issued = i;
         }
     } else if (warp == 2) {
         if (lane == 0) {
@@ -177,7 +173,7 @@ __global__ void __launch_bounds__(kRmThreads, 1) pf_router_mma_kernel(const __gr
                 }
             }
             umma::commit(mdone);
-            mbar_drain(mdone, 0u, p.wait_ns);
+            mbar_drain(mdone, 0u, globaltimer());
         }
     } else if (warp >= 4) {
         // epilogue: lane quadrant (warp - 4), lane = expert row of the tile
@@ -224,6 +220,7 @@ __global__ void __launch_bounds__(kRmThreads, 1) pf_router_mma_kernel(const __gr
     }
     umma::fence_before();
     __syncthreads();
+    if (warp == 1 && lane == 0 && *s_abort) drain_ring(full, kRmStages, issued);
     if (warp == 0) {
         umma::fence_after();
         umma::tmem_dealloc(tbase, kCols);

@@ -147,6 +147,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) pf_expert_kernel(const __grid_c
         if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&mempty[q % kPfSlots])) : "memory");
     };
 
+    int issued = 0;  // stages filled (the copying warp)
     if (warp == 10) {
         // ---------------------------------------------- group descriptions --
         // Two items in flight: the record of item q+2 and the pairs of item
@@ -265,14 +266,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) pf_expert_kernel(const __grid_c
             }
             slot_done(q);
         }
-        if (*s_abort && lane == 0) {
-            // wait (bounded) for the last copy issued into each stage, so none
-            // lands after the CTA's shared memory is released
-            for (int q = 0; q < nst && q < it_stage; ++q) {
-                const int last = q + ((it_stage - 1 - q) / nst) * nst;
-                mbar_drain(&full[q], (uint32_t)((last / nst) & 1), p.wait_ns);
-            }
-        }
+        issued = it_stage;
     } else if (warp >= 4 && warp < 8) {
         // --------------------------------------- scale factors -> TMEM --
         const uint32_t lb = umma::lane_base(warp);
@@ -502,7 +496,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) pf_expert_kernel(const __grid_c
         // has completed (on an early exit too)
         if (umma::elect()) {
             umma::commit(mdone);
-            mbar_drain(mdone, 0u, p.wait_ns);
+            mbar_drain(mdone, 0u, globaltimer());
         }
     } else {
         // --------------------------------------------------- epilogue --
@@ -636,6 +630,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) pf_expert_kernel(const __grid_c
     }
     umma::fence_before();
     __syncthreads();
+    if (warp == 8 && lane == 0 && *s_abort) drain_ring(full, nst, issued);
     if (warp == 0) {
         umma::fence_after();
         umma::tmem_dealloc(tbase, kCols);

@@ -545,6 +545,7 @@ __global__ void __launch_bounds__(kUThreads, 1) umma_expert_kernel(const __grid_
         return y;
     };
 
+    int issued = 0;  // stages filled (the copying warp)
     if (warp == 8) {
         // ------------------------------------------------ TMA producer --
         // Warp-uniform loops, one elected lane issues (as the MMA warp): with
@@ -665,15 +666,7 @@ __global__ void __launch_bounds__(kUThreads, 1) umma_expert_kernel(const __grid_
             pdl_wait();
             if (lane == 0) hdr->prep_done = 0u;
         }
-        if (*s_abort && lane == 0) {
-            // a wait gave up somewhere: wait (bounded) for the last copy
-            // issued into each stage, so none lands after the CTA's
-            // shared memory is released
-            for (int q = 0; q < nst && q < it; ++q) {
-                const int last = q + ((it - 1 - q) / nst) * nst;  // its last use
-                mbar_drain(&full[q], (uint32_t)((last / nst) & 1), p.wait_ns);
-            }
-        }
+        issued = it;
     } else if (warp >= 4 && warp < 8) {
         // --------------------------------------- scale factors -> TMEM --
         const uint32_t lb = umma::lane_base(warp);
@@ -908,7 +901,7 @@ __global__ void __launch_bounds__(kUThreads, 1) umma_expert_kernel(const __grid_
         // has completed (on an early exit too)
         if (umma::elect()) {
             umma::commit(mdone);
-            mbar_drain(mdone, 0u, p.wait_ns);
+            mbar_drain(mdone, 0u, globaltimer());
         }
     } else if (warp < 4) {
         // --------------------------------------------------- epilogue --
@@ -1089,6 +1082,7 @@ __global__ void __launch_bounds__(kUThreads, 1) umma_expert_kernel(const __grid_
     }
     umma::fence_before();
     __syncthreads();
+    if (warp == 8 && lane == 0 && *s_abort) drain_ring(full, nst, issued);
     if (warp == 0) {
         umma::fence_after();
         umma::tmem_dealloc(tbase, kCols);
