@@ -602,7 +602,11 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
                                    umma::mapa(smem_u32(rfull), threadIdx.x));
             }
             __syncwarp();
-            if (jmax > 0) wait(rfull, 0u);
+            // Every CTA sends, one that gave up too: what is sent here lands
+            // before this CTA leaves (the cluster barrier orders the sending,
+            // not the landing).
+            if (jmax > 0 && !wait(rfull, 0u)) mbar_drain(rfull, 0u, globaltimer());
+            __syncwarp();
         }
         const float *own = part + rank * cpo * 128 + (n - n0);
         if (n < p.N) {

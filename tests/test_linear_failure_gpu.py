@@ -73,3 +73,11 @@ def test_few_tokens(T, n, k, gated, fp32):
 @pytest.mark.parametrize("T,n,k", [(40, 200, 64), (40, 200, 128), (130, 300, 136)])  # too short to be split
 def test_tiles(T, n, k, gated, fp32):
     runs_out_and_recovers(T, n, k, gated, fp32)
+
+
+@pytest.mark.parametrize("gated,fp32", [(False, True), (True, False), (True, True)])
+@pytest.mark.parametrize("T,n,k", [(64, 896, 7168), (100, 1536, 7168), (40, 130, 20000), (129, 65, 9000)])
+def test_split_reductions(T, n, k, gated, fp32):
+    """One CTA of each cluster gives up; the others get its part late or not in
+    time, and leave only after it has landed."""
+    runs_out_and_recovers(T, n, k, gated, fp32)
