@@ -807,7 +807,6 @@ __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid
             if (umma::elect()) umma::commit_pair(mdone);
             __syncwarp();
         }
-        wait(mdone, 0u);  // in both CTAs: the last arrival from the pair's MMAs
     } else {
         // Epilogue: warp w takes lane quadrant w % 4 and every fourth group of
         // 16 tokens, through shared memory so that a thread finishes 8
@@ -949,6 +948,11 @@ __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid
             }
         }
     }
+    // Every role of this CTA is done: only now the wait for the last arrival
+    // from the pair's MMAs, in both CTAs.  From the start its limit would be
+    // one on the whole call.
+    __syncthreads();
+    if (warp == kLpEpi + 1) mbar_drain(mdone, 0u, globaltimer());
     __syncwarp();
     umma::fence_before();
     umma::cluster_arrive();

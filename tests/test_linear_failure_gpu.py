@@ -81,3 +81,20 @@ def test_split_reductions(T, n, k, gated, fp32):
     """One CTA of each cluster gives up; the others get its part late or not in
     time, and leave only after it has landed."""
     runs_out_and_recovers(T, n, k, gated, fp32)
+
+
+@pytest.mark.parametrize("gated,fp32", [(False, False), (True, False), (False, True)])
+def test_a_wait_bounds_a_step_and_not_the_call(gated, fp32):
+    """Some 5 ms of work in steps of 0.05 ms at most: with 1 ms for each wait
+    nothing runs out, and every tile is written."""
+    T, n, k = 65536, 3584 if gated else 7168, 7168
+    run, ws = product(T, n, k, gated, fp32)
+    want, status = run()
+    assert status == m.K3MOE_OK
+    try:
+        assert m.k3moe_debug_set_fault(0, 1_000_000) == m.K3MOE_OK
+        got, status = run()
+    finally:
+        m.k3moe_debug_set_fault(0, 0)
+    assert status == m.K3MOE_OK
+    assert torch.equal(got, want)
