@@ -683,6 +683,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid
     uint64_t *mdone = aempty + 2;
     uint32_t *tslot = reinterpret_cast<uint32_t *>(mdone + 1);
     volatile int *s_abort = reinterpret_cast<volatile int *>(tslot + 1);
+    volatile int *s_issued = s_abort + 1;  // stages that this CTA's copies filled
     uint8_t *stages = smem + kLtHead;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)umma::cluster_rank();
@@ -742,7 +743,8 @@ __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid
             int n0, t0;
             const int tn = tile_at(it, n0, t0), tx = t0 + rank * (tn / 2);
             const void *xmap = it < a.whole ? a.tx : a.tx_part;
-            for (int kt = 0; kt < nk; ++kt, ++i) {
+            const int fill = a.inject && rank == 1 && it + pairs >= items ? nk - 1 : nk;
+            for (int kt = 0; kt < fill; ++kt, ++i) {
                 if (!wait(&empty[s], ph)) {
                     ok = false;
                     break;
@@ -762,9 +764,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid
                 }
             }
         }
-        if (*s_abort && rank == 0 && lane == 0) {
-            drain_ring(full, nst, i);
-        }
+        if (lane == 0) *s_issued = i;
     } else if (warp == kLpEpi + 1) {
         if (rank == 0) {
             const uint64_t adesc = umma::smem_desc(smem_u32(stages), 16u, 1024u, umma::kLayoutSw128);
@@ -948,6 +948,8 @@ __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid
             }
         }
     }
+    // a CTA that gave up tells the other one, whose waits then end too
+    if (lane == 0 && *s_abort) umma::st_cluster(umma::mapa(smem_u32(const_cast<int *>(s_abort)), (uint32_t)(rank ^ 1)), 1u);
     // Every role of this CTA is done: only now the wait for the last arrival
     // from the pair's MMAs, in both CTAs.  From the start its limit would be
     // one on the whole call.
@@ -957,6 +959,28 @@ __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid
     umma::fence_before();
     umma::cluster_arrive();
     umma::cluster_wait();  // neither CTA leaves while the other's copies, MMAs or arrivals need it
+    if (*s_abort) {
+        // Alike in both CTAs from here on.  CTA 0's barriers count the copies of both: it
+        // takes off what a CTA that stopped earlier will not bring, and waits
+        // for the rest before either CTA leaves.
+        if (warp == kLpEpi + 1) mbar_drain(mdone, 0u, globaltimer());
+        if (warp == kLpEpi && rank == 0 && lane == 0) {
+            const uint64_t t0 = globaltimer();
+            const int i0 = *s_issued, i1 = (int)umma::ld_cluster(umma::mapa(smem_u32(const_cast<int *>(s_issued)), 1u));
+            const int end = max(i0, i1);
+            for (int j = max(0, end - nst); j < end; ++j) {
+                const int s = j % nst;
+                int n0, t;
+                const uint32_t bytes = (uint32_t)(kLtA + tile_at(pair + j / nk * pairs, n0, t) * 64);  // of one CTA
+                if (j >= i1) umma::complete_tx(&full[s], bytes);
+                if (j >= i0) mbar_arrive_expect_tx(&full[s], bytes);
+                mbar_drain(&full[s], (uint32_t)((j / nst) & 1), t0);
+            }
+        }
+        __syncwarp();
+        umma::cluster_arrive();
+        umma::cluster_wait();
+    }
     if (warp == 0) {
         umma::fence_after();
         umma::tmem_dealloc_pair(tbase, 512u);

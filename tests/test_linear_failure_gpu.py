@@ -98,3 +98,10 @@ def test_a_wait_bounds_a_step_and_not_the_call(gated, fp32):
         m.k3moe_debug_set_fault(0, 0)
     assert status == m.K3MOE_OK
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("gated,fp32", [(False, False), (True, False), (False, True), (True, True)])
+@pytest.mark.parametrize("T,n,k", [(4096, 4104, 72), (2047, 2500, 520), (4095, 2304, 1096), (1500, 3001, 584)])
+def test_pairs(T, n, k, gated, fp32):
+    """One CTA of each pair stops a copy short of the other."""
+    runs_out_and_recovers(T, n, k, gated, fp32)
