@@ -800,7 +800,7 @@ __global__ void __launch_bounds__(kUThreads, 1) umma_expert_kernel(const __grid_
         bool go = true;
         int done = 0;  // stages passed in earlier ranges
         for (int ri = 0; ri < 2 && go; ++ri) {
-            if (ri == 1 && (!GU || !routed_range())) break;
+            if (ri == 1 && (!GU || !umma::bar_red_and(2, 128, routed_range()))) break;  // together, as in store
             const Range rg = rng(ri);
             const int a = rg.a, n = rg.b - rg.a;
 #pragma unroll
@@ -912,7 +912,9 @@ __global__ void __launch_bounds__(kUThreads, 1) umma_expert_kernel(const __grid_
                          (GU ? 0 : L.umax * ceil_div(p.ff, kTileM) + ceil_div(L.ffs, kTileM));
         int seg = 0;
         for (int ri = 0; ri < 2; ++ri) {
-        if (ri == 1 && (!GU || !routed_range())) break;
+        // the four warps go on together or not at all (named barriers below):
+        // one that meets a role's giving up here must not leave the others
+        if (ri == 1 && (!GU || !umma::bar_red_and(1, 128, routed_range()))) break;
         const Range rg = rng(ri);
         for (int unit = rg.a; unit < rg.b; ++seg) {
             const Unit x = decode(unit);
