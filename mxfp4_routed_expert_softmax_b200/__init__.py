@@ -4,7 +4,10 @@ streams, every step of the layer runs in the library's CUDA kernels.  The
 C contract of each call is documented in include/k3moe.h.  k3moe_gate,
 k3moe_linear and k3moe_layer_routed go through a compiled module
 (csrc/py_binding.cpp), which refuses tensors that are not in the current
-device's memory; the other calls go through ctypes.
+device's memory, of another type (16-bit integers may hold the bits of bf16),
+smaller than the call's T and descriptor say, or with strides that the call
+cannot express; the other calls go through ctypes and take addresses as they
+are.
 
 The library is loaded at import time; if it has not been built (``python
 mxfp4_routed_expert_softmax_b200/build.py``) the import fails loudly -- there is
@@ -270,12 +273,14 @@ if "torch" in sys.modules:
 
 
 def k3moe_gate(logits, T, bias, gate, idx, weight, stream=None) -> int:
-    """logits: [T, E] tensor (rows may be a slice of wider ones) or an address."""
+    """logits: [T, E] tensor (rows may be a slice of wider ones) or an address;
+    the other tensors contiguous.  Every tensor may have more rows than T."""
     return (_binding or _load_binding()).gate(logits, T, bias, gate, idx, weight, stream)
 
 
 def k3moe_layer_routed(x, T, idx, weight, expert_blobs, shared_wg, shared_wu, shared_wd, dims, y, ws,
                        ws_bytes=None, stream=None) -> int:
+    """Every tensor contiguous, of any shape that holds enough elements."""
     return (_binding or _load_binding()).layer_routed(x, T, idx, weight, expert_blobs, shared_wg, shared_wu, shared_wd,
                                                       dims, y, ws, ws_bytes, stream)
 

@@ -30,18 +30,39 @@ bool address(PyObject *o, void **out) {
     return true;
 }
 
+// What an operand's elements are.  bf16 tensors may also be integer ones that
+// hold the bits.
+enum Kind { kBf16, kFp32, kInt32, kPointer };
+bool is(const at::Tensor *t, Kind kind) {
+    const at::ScalarType s = t->scalar_type();
+    switch (kind) {
+        case kBf16: return s == at::kBFloat16 || s == at::kShort || s == at::kUInt16;
+        case kFp32: return s == at::kFloat;
+        case kInt32: return s == at::kInt;
+        default: return s == at::kLong || s == at::kUInt64;
+    }
+}
+
 // Row distance of a 2-D operand given as a tensor (0: an address or none,
 // rows without gaps); -1, which means an invalid argument, when the tensor is
-// not `cols` wide with consecutive elements of `size` bytes.
-int64_t rows(PyObject *o, size_t size, int64_t cols) {
+// not `cols` wide with consecutive elements of this kind, or has fewer than
+// `n` rows.
+int64_t rows(PyObject *o, Kind kind, int64_t n, int64_t cols) {
     const at::Tensor *t = tensor_of(o);
     if (!t) return 0;
     const int64_t dim = t->dim();
-    if (dim < 1 || dim > 2 || t->element_size() != (int64_t)size || t->size(dim - 1) != cols ||
-        (cols > 1 && t->stride(dim - 1) != 1))
-        return -1;
-    if (dim == 1 || t->size(0) == 1) return cols;
+    if (dim < 1 || dim > 2 || !is(t, kind) || t->size(dim - 1) != cols || (cols > 1 && t->stride(dim - 1) != 1)) return -1;
+    const int64_t have = dim == 1 ? 1 : t->size(0);
+    if (have < n) return -1;
+    if (have <= 1) return cols;
     return t->stride(0) >= cols ? t->stride(0) : -1;
+}
+
+// Whether an operand (a tensor; an address is taken as it is) is contiguous
+// with at least n elements of this kind.
+bool flat(PyObject *o, Kind kind, int64_t n) {
+    const at::Tensor *t = tensor_of(o);
+    return !t || (is(t, kind) && t->is_contiguous() && t->numel() >= n);
 }
 
 // Whether every tensor among the arguments is in the current device's memory
@@ -55,12 +76,6 @@ bool on_device(PyObject *const *a, Py_ssize_t n) {
             if (t->device().index() != device) return false;
         }
     return true;
-}
-
-// Whether a tensor is contiguous with elements of 4 bytes.
-bool flat4(PyObject *o) {
-    const at::Tensor *t = tensor_of(o);
-    return !t || (t->element_size() == 4 && t->is_contiguous());
 }
 
 bool stream_of(PyObject *o, void **out) {
@@ -116,6 +131,10 @@ bool bytes_of(PyObject *ws, PyObject *given, size_t *out) {
     *out = t->nbytes();
     return true;
 }
+bool holds(PyObject *ws, size_t bytes) {
+    const at::Tensor *t = tensor_of(ws);
+    return !t || (t->is_contiguous() && t->nbytes() >= bytes);
+}
 
 bool count(Py_ssize_t n, Py_ssize_t want) {
     if (n == want) return true;
@@ -143,8 +162,10 @@ PyObject *gate(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (!count(n, 7) || !address(a[0], &logits) || !int32_of(a[1], &T) || !address(a[2], &bias) || !descriptor(a[3], &d) ||
         !address(a[4], &idx) || !address(a[5], &weight) || !stream_of(a[6], &stream))
         return nullptr;
-    const int64_t ld = rows(a[0], d->flags & K3MOE_LOGITS_BF16 ? 2 : 4, d->n_experts);
-    if (!on_device(a, 6) || ld < 0 || !flat4(a[2]) || !flat4(a[4]) || !flat4(a[5])) return status(K3MOE_ERR_INVALID_ARGUMENT);
+    const int64_t ld = rows(a[0], d->flags & K3MOE_LOGITS_BF16 ? kBf16 : kFp32, T, d->n_experts), picks = (int64_t)T * d->top_k;
+    if (!on_device(a, 6) || ld < 0 || !flat(a[2], kFp32, d->n_experts) || !flat(a[4], kInt32, picks) ||
+        !flat(a[5], kFp32, picks))
+        return status(K3MOE_ERR_INVALID_ARGUMENT);
     return call(g_gate, logits, ld, T, static_cast<const float *>(bias), d, static_cast<int32_t *>(idx),
                 static_cast<float *>(weight), stream);
 }
@@ -159,10 +180,11 @@ PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
         !address(a[4], &b) || !address(a[5], &bg) || !address(a[6], &r) || !descriptor(a[7], &d) || !address(a[8], &out) ||
         !address(a[9], &ws) || !bytes_of(a[9], a[10], &bytes) || !stream_of(a[11], &stream))
         return nullptr;
-    const size_t osz = d->flags & K3MOE_OUT_FP32 ? 4 : 2;
-    const int64_t ldx = rows(a[0], 2, d->k), ldw = rows(a[2], 2, d->k), ldr = rows(a[6], osz, d->n), ldo = rows(a[8], osz, d->n);
-    if (!on_device(a, 10) || ldx < 0 || ldw < 0 || ldr < 0 || ldo < 0 || !flat4(a[4]) || !flat4(a[5]) ||
-        (a[3] != Py_None && rows(a[3], 2, d->k) != ldw))
+    const Kind kind = d->flags & K3MOE_OUT_FP32 ? kFp32 : kBf16;
+    const int64_t ldx = rows(a[0], kBf16, T, d->k), ldw = rows(a[2], kBf16, d->n, d->k), ldr = rows(a[6], kind, T, d->n),
+                  ldo = rows(a[8], kind, T, d->n);
+    if (!on_device(a, 10) || ldx < 0 || ldw < 0 || ldr < 0 || ldo < 0 || !flat(a[4], kFp32, d->n) ||
+        !flat(a[5], kFp32, d->n) || (a[3] != Py_None && rows(a[3], kBf16, d->n, d->k) != ldw) || !holds(a[9], bytes))
         return status(K3MOE_ERR_INVALID_ARGUMENT);
     return call(g_linear, x, ldx, T, w, wg, ldw, static_cast<const float *>(b), static_cast<const float *>(bg), r, ldr, d, out,
                 ldo, ws, bytes, stream);
@@ -179,7 +201,15 @@ PyObject *layer_routed(PyObject *, PyObject *const *a, Py_ssize_t n) {
         !descriptor(a[8], &d) || !address(a[9], &y) || !address(a[10], &ws) || !bytes_of(a[10], a[11], &bytes) ||
         !stream_of(a[12], &stream))
         return nullptr;
-    if (!on_device(a, 11) || !flat4(a[2]) || !flat4(a[3])) return status(K3MOE_ERR_INVALID_ARGUMENT);
+    // The library takes x, y and the shared matrices as dense: a slice of wider
+    // rows is refused, not misread.
+    const int64_t td = (int64_t)T * d->d, picks = (int64_t)T * d->top_k, mat = (int64_t)d->ff_shared * d->d;
+    const bool shared = !(d->flags & K3MOE_NO_SHARED);
+    if (!on_device(a, 11) || !flat(a[0], kBf16, td) || !flat(a[2], kInt32, picks) || !flat(a[3], kFp32, picks) ||
+        !flat(a[4], kPointer, d->n_experts) ||
+        (shared && (!flat(a[5], kBf16, mat) || !flat(a[6], kBf16, mat) || !flat(a[7], kBf16, mat))) ||
+        !flat(a[9], d->flags & K3MOE_OUT_FP32 ? kFp32 : kBf16, td) || !holds(a[10], bytes))
+        return status(K3MOE_ERR_INVALID_ARGUMENT);
     return call(g_routed, x, T, static_cast<const int32_t *>(idx), static_cast<const float *>(weight),
                 static_cast<const uint8_t *const *>(blobs), sg, su, sd, d, y, ws, bytes, stream);
 }
