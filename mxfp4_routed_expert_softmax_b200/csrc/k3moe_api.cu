@@ -873,7 +873,7 @@ k3moe_status check_linear(const k3moe_linear_desc *l) {
 // A warp per token, the logits of a lane in 4 * ceil(E / 128) registers.
 template <int NI>
 cudaError_t launch_gate_ni(const GateParams &p, cudaStream_t st) {
-    const dim3 grid((unsigned)ceil_div(p.T, kGateWarps)), block(32 * kGateWarps);
+    const dim3 grid(((unsigned)p.T + kGateWarps - 1u) / kGateWarps), block(32 * kGateWarps);  // unsigned: any T
     const size_t smem = gate_smem(NI);
     return p.bias ? launch(gate_kernel<NI, true>, grid, block, smem, st, true, p)
                   : launch(gate_kernel<NI, false>, grid, block, smem, st, true, p);
