@@ -11,7 +11,8 @@ are.
 
 The library is loaded at import time; if it has not been built (``python
 mxfp4_routed_expert_softmax_b200/build.py``) the import fails loudly -- there is
-no fallback implementation.
+no fallback implementation.  Without the compiled module (it is built for one
+torch) those three calls raise ImportError, and the others work.
 """
 from __future__ import annotations
 
@@ -251,17 +252,23 @@ def k3moe_layer_timed(x, T, w_router, bias, expert_blobs, shared_wg, shared_wu, 
 
 def _load_binding():
     """The compiled entry points of the calls below (csrc/py_binding.cpp): they
-    read the tensors' addresses and strides themselves.  Needs torch."""
+    read the tensors' addresses and strides themselves.  Needs torch, and a
+    module built against this one."""
     global _binding
     import torch  # noqa: F401  (its libraries, before the module that links them)
-    path = os.path.join(_PKG, "_binding.so")
-    if not os.path.exists(path):
-        raise ImportError(f"{path} is missing: build it with "
-                          "`python mxfp4_routed_expert_softmax_b200/build.py`")
-    import importlib.util
-    spec = importlib.util.spec_from_file_location("_binding", path)
-    mod = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(mod)
+
+    from .build import binding_path
+    path = binding_path()
+    try:
+        if not os.path.exists(path):
+            raise ImportError("no such file")
+        import importlib.util
+        spec = importlib.util.spec_from_file_location("_binding", path)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+    except ImportError as e:
+        raise ImportError(f"k3moe_gate, k3moe_linear and k3moe_layer_routed need {path} ({e}): build it with "
+                          "`python mxfp4_routed_expert_softmax_b200/build.py`") from e
     mod.bind(*(ctypes.cast(f, _vp).value for f in (lib.k3moe_gate, lib.k3moe_linear, lib.k3moe_layer_routed)))
     _binding = mod
     return mod
@@ -269,7 +276,10 @@ def _load_binding():
 
 _binding = None
 if "torch" in sys.modules:
-    _load_binding()
+    try:
+        _load_binding()
+    except ImportError:
+        pass  # the calls that need it raise it; the others go through ctypes
 
 
 def k3moe_gate(logits, T, bias, gate, idx, weight, stream=None) -> int:
