@@ -447,6 +447,7 @@ __global__ void __launch_bounds__(kLThreads, 1) layer_kernel(const __grid_consta
     volatile int *s_last = s_abort + 2;
     volatile int *s_rdone = s_abort + 3;  // router rows this CTA finished
     volatile int *s_rok = s_abort + 4;    // every router row is in (top-k warps)
+    volatile int *s_issued = s_abort + 5;  // stages filled, once all are; -1 before
     int *s_r0c = const_cast<int *>(s_abort) + 8;  // [stage]: warps done with a router unit
     const uint8_t **s_ptab = reinterpret_cast<const uint8_t **>(tail + so.ptab);
     const uint8_t **s_blob = reinterpret_cast<const uint8_t **>(tail + so.blob);
@@ -480,6 +481,7 @@ __global__ void __launch_bounds__(kLThreads, 1) layer_kernel(const __grid_consta
         mbar_init(tkpart, 4);
         fence_mbar_init();
         *s_abort = 0;
+        *s_issued = -1;
         *s_U = 0;
         *s_rdone = 0;
         for (int q = 0; q < 8; ++q) s_r0c[q] = 0;
@@ -792,7 +794,6 @@ __global__ void __launch_bounds__(kLThreads, 1) layer_kernel(const __grid_consta
         }
     }
 
-    int issued = 0;  // stages filled (the copying thread)
     if (warp == 8) {
         // ========================================================= copies --
         if (lane == 0) {
@@ -941,7 +942,7 @@ __global__ void __launch_bounds__(kLThreads, 1) layer_kernel(const __grid_consta
                 for (int q = 0; q < npend; ++q) issue_b(pend_s[q], decode(3, pend_unit[q]));
                 npend = 0;
             }
-            issued = i;
+            *s_issued = i;
         }
     } else if (warp >= 4 && warp < 8) {
         // ============================ router sums (R0), scales -> TMEM =====
@@ -1214,6 +1215,7 @@ __global__ void __launch_bounds__(kLThreads, 1) layer_kernel(const __grid_consta
             }
         }
         if (p.strict && __any_sync(0xffffffffu, nanb != 0u) && lane == 0) set_status(hdr, kStDeviceCheck);
+        if (warp == 4 && lane == 0 && *s_abort) drain_ring(full, nst, s_issued);  // the router units' copies
     } else if (warp == 9) {
         // ====================================================== MMA issue --
         if (lane == 0) {
@@ -1330,6 +1332,7 @@ __global__ void __launch_bounds__(kLThreads, 1) layer_kernel(const __grid_consta
             // has completed (on an early exit too)
             umma::commit(mdone);
             mbar_drain(mdone, 0u, globaltimer());
+            if (*s_abort) drain_ring(full, nst, s_issued);
         }
     }
 
@@ -1502,7 +1505,6 @@ __global__ void __launch_bounds__(kLThreads, 1) layer_kernel(const __grid_consta
 
     umma::fence_before();
     __syncthreads();
-    if (warp == 8 && lane == 0 && *s_abort) drain_ring(full, nst, issued);
     if (warp == 0) {
         umma::fence_after();
         umma::tmem_dealloc(tbase, kCols);

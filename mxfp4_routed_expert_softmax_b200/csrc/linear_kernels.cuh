@@ -333,7 +333,10 @@ __global__ void __launch_bounds__(32 * kLsWarps) linear_stream_kernel(const __gr
         __syncwarp();
     }
     // a warp that gave up waits (bounded) for its own copies in flight
-    if (!ok && lane == 0) drain_ring(bar, a.ns, issued);
+    if (!ok && lane == 0) {
+        const uint64_t t0 = globaltimer();
+        for (int i = 0; i < a.ns && i < issued; ++i) mbar_drain(&bar[i], (uint32_t)(((issued - 1 - i) / a.ns) & 1), t0);
+    }
 }
 
 // -------------------------------------------------------- tcgen05 kernels --
@@ -402,6 +405,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
     uint64_t *rfull = mdone + 1;  // the other CTAs' parts of this CTA's columns have arrived
     uint32_t *tslot = reinterpret_cast<uint32_t *>(rfull + 1);
     volatile int *s_abort = reinterpret_cast<volatile int *>(tslot + 1);
+    volatile int *s_issued = s_abort + 1;  // stages filled, once all are; -1 before
     uint8_t *stages = smem + kLtHead;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -417,6 +421,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
         mbar_init(rfull, 1);
         fence_mbar_init();
         *s_abort = 0;
+        *s_issued = -1;
     }
     if (warp == kLtEpi && lane == 0) {
         umma::prefetch_tmap(a.tw);
@@ -437,6 +442,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
     const int n0 = (tile % a.nrb) * nrow, t0 = (tile / a.nrb) * bn;
     const int nkt = ceil_div(p.K, kLtKStep);
     const int kt0 = (int)((long long)nkt * rank / S), nk = (int)((long long)nkt * (rank + 1) / S) - kt0;
+    const int fill = a.inject && rank == 0 ? nk - 1 : nk;  // K-steps copied
     const int nch = ceil_div(nk, a.chain);
     const int cpo = ceil_div(bn, S);  // columns that one CTA of the cluster finishes
     auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait_warp(bar, parity, a.hdr, a.wait_ns, s_abort); };
@@ -450,11 +456,9 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
     const int cend = min(bn, p.T - t0);                     // columns that exist
     const int jmax = max(0, min(cpo, cend - rank * cpo));   // of them, finished here
     if (S > 1 && threadIdx.x == 0 && jmax > 0) mbar_arrive_expect_tx(rfull, (uint32_t)((S - 1) * jmax * 512));
-    int issued = 0;  // stages filled (the copying warp)
     if (warp == kLtEpi) {
         int i = 0, s = 0;
         uint32_t ph = 1u;  // of the empty barriers: the first round's waits pass at once
-        const int fill = a.inject && rank == 0 ? nk - 1 : nk;
         for (; i < fill; ++i) {
             if (!wait(&empty[s], ph)) break;
             if (umma::elect()) {
@@ -471,7 +475,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
                 ph ^= 1u;
             }
         }
-        issued = i;
+        if (lane == 0) *s_issued = i;
     } else if (warp == kLtEpi + 1) {
         const uint64_t adesc = umma::smem_desc(smem_u32(stages), 16u, 1024u, umma::kLayoutSw128);
         const uint32_t idesc = umma::idesc_bf16(bn);
@@ -509,6 +513,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
         if (umma::elect()) {
             umma::commit(mdone);
             mbar_drain(mdone, 0u, globaltimer());
+            if (*s_abort) drain_ring(full, nst, s_issued);
         }
     } else {
         // A thread finishes 4 columns of the tokens j0, j0 + step, ... of its
@@ -643,7 +648,6 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
     }
     umma::fence_before();
     __syncthreads();
-    if (warp == kLtEpi && lane == 0 && *s_abort) drain_ring(full, nst, issued);
     if (warp == 0) {
         umma::fence_after();
         umma::tmem_dealloc(tbase, (uint32_t)a.tcols);
@@ -667,6 +671,30 @@ constexpr int kLpEpi = 16;                  // epilogue warps: four per lane qua
 constexpr int kLpThreads = 32 * (kLpEpi + 2);
 constexpr int kLpExch = kLpEpi * 16 * kLpRow * 4;
 
+// drain_ring for a pair, by CTA 0's issuing role: its barriers count the copies
+// of both CTAs.  What a CTA that stopped earlier will not bring is taken off,
+// and the rest waited for.  CTA 1 is told to give up, and is still there (the
+// closing cluster barrier).  Not inlined: in the kernel's body it changed the
+// code of the loops (4095 x 7168 x 1536 with a residual 72 us, 78 with it).
+__device__ __noinline__ void pair_drain(uint64_t *full, int nst, volatile int *issued, int nk, int whole, int bn, int parts) {
+    const uint32_t there = umma::mapa(smem_u32(const_cast<int *>(issued)), 1u);
+    umma::st_cluster(there - 4, 1u);  // its s_abort, the word before
+    uint64_t t0 = globaltimer();
+    int i0, i1;
+    while ((i0 = *issued) < 0 || (i1 = (int)umma::ld_cluster(there)) < 0) {
+        if (globaltimer() - t0 > 2 * kWaitLimitNs) return;
+    }
+    t0 = globaltimer();
+    const int pairs = gridDim.x >> 1, end = max(i0, i1);
+    for (int j = max(0, end - nst); j < end; ++j) {
+        const int s = j % nst, it = (int)(blockIdx.x >> 1) + j / nk * pairs;
+        const uint32_t bytes = (uint32_t)(kLtA + (it < whole ? bn : bn / parts) * 64);  // of one CTA
+        if (j >= i1) umma::complete_tx(&full[s], bytes);
+        if (j >= i0) mbar_arrive_expect_tx(&full[s], bytes);
+        mbar_drain(&full[s], (uint32_t)((j / nst) & 1), t0);
+    }
+}
+
 // OUT32: the output's type.  VEC: p.vec (a choice at run time cost the aligned
 // case 2 to 4 us: 1024 x 7168 x 1536 with a residual 24.5 us, 28.3 with it).
 template <bool GATED, bool RESID, bool VEC, bool OUT32>
@@ -683,7 +711,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid
     uint64_t *mdone = aempty + 2;
     uint32_t *tslot = reinterpret_cast<uint32_t *>(mdone + 1);
     volatile int *s_abort = reinterpret_cast<volatile int *>(tslot + 1);
-    volatile int *s_issued = s_abort + 1;  // stages that this CTA's copies filled
+    volatile int *s_issued = s_abort + 1;  // stages that this CTA's copies filled, once all are; -1 before
     uint8_t *stages = smem + kLtHead;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)umma::cluster_rank();
@@ -699,6 +727,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid
         mbar_init(mdone, 1);
         fence_mbar_init();
         *s_abort = 0;
+        *s_issued = -1;
     }
     if (warp == kLpEpi && lane == 0) {
         umma::prefetch_tmap(a.tw);
@@ -804,7 +833,10 @@ __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid
                     it += pairs;
                 }
             }
-            if (umma::elect()) umma::commit_pair(mdone);
+            if (umma::elect()) {
+                umma::commit_pair(mdone);
+                if (*s_abort) pair_drain(full, nst, s_issued, nk, a.whole, a.bn, a.parts);
+            }
             __syncwarp();
         }
     } else {
@@ -948,39 +980,15 @@ __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid
             }
         }
     }
-    // a CTA that gave up tells the other one, whose waits then end too
-    if (lane == 0 && *s_abort) umma::st_cluster(umma::mapa(smem_u32(const_cast<int *>(s_abort)), (uint32_t)(rank ^ 1)), 1u);
     // Every role of this CTA is done: only now the wait for the last arrival
     // from the pair's MMAs, in both CTAs.  From the start its limit would be
-    // one on the whole call.
+    // one on the whole call.  (The other CTA may have two limits to go.)
     __syncthreads();
-    if (warp == kLpEpi + 1) mbar_drain(mdone, 0u, globaltimer());
+    if (warp == kLpEpi + 1) mbar_drain(mdone, 0u, globaltimer(), 4 * kWaitLimitNs);
     __syncwarp();
     umma::fence_before();
     umma::cluster_arrive();
     umma::cluster_wait();  // neither CTA leaves while the other's copies, MMAs or arrivals need it
-    if (*s_abort) {
-        // Alike in both CTAs from here on.  CTA 0's barriers count the copies of both: it
-        // takes off what a CTA that stopped earlier will not bring, and waits
-        // for the rest before either CTA leaves.
-        if (warp == kLpEpi + 1) mbar_drain(mdone, 0u, globaltimer());
-        if (warp == kLpEpi && rank == 0 && lane == 0) {
-            const uint64_t t0 = globaltimer();
-            const int i0 = *s_issued, i1 = (int)umma::ld_cluster(umma::mapa(smem_u32(const_cast<int *>(s_issued)), 1u));
-            const int end = max(i0, i1);
-            for (int j = max(0, end - nst); j < end; ++j) {
-                const int s = j % nst;
-                int n0, t;
-                const uint32_t bytes = (uint32_t)(kLtA + tile_at(pair + j / nk * pairs, n0, t) * 64);  // of one CTA
-                if (j >= i1) umma::complete_tx(&full[s], bytes);
-                if (j >= i0) mbar_arrive_expect_tx(&full[s], bytes);
-                mbar_drain(&full[s], (uint32_t)((j / nst) & 1), t0);
-            }
-        }
-        __syncwarp();
-        umma::cluster_arrive();
-        umma::cluster_wait();
-    }
     if (warp == 0) {
         umma::fence_after();
         umma::tmem_dealloc_pair(tbase, 512u);

@@ -88,6 +88,7 @@ __global__ void __launch_bounds__(kRmThreads, 1) pf_router_mma_kernel(const __gr
     uint64_t *mdone = aempty + 2;
     uint32_t *tslot = reinterpret_cast<uint32_t *>(mdone + 1);
     volatile int *s_abort = reinterpret_cast<volatile int *>(tslot + 1);
+    volatile int *s_issued = s_abort + 1;  // stages filled, once all are; -1 before
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     WsHeader *hdr = reinterpret_cast<WsHeader *>(p.ws);
     if (threadIdx.x == 0) {
@@ -102,6 +103,7 @@ __global__ void __launch_bounds__(kRmThreads, 1) pf_router_mma_kernel(const __gr
         mbar_init(mdone, 1);
         fence_mbar_init();
         *s_abort = 0;
+        *s_issued = -1;
     }
     constexpr uint32_t kCols = 256u;
     if (warp == 0) umma::tmem_alloc(tslot, kCols);
@@ -118,7 +120,6 @@ __global__ void __launch_bounds__(kRmThreads, 1) pf_router_mma_kernel(const __gr
         *s_abort = 1;
         return false;
     };
-    int issued = 0;  // stages filled (the copying thread)
     if (warp == 1) {
         if (lane == 0) {
             int i = 0;
@@ -134,7 +135,7 @@ __global__ void __launch_bounds__(kRmThreads, 1) pf_router_mma_kernel(const __gr
                     umma::tma_load_2d(st + 3 * kRmBox, p.tx, ks * kRmKStep, t0, &full[s]);
                 }
             }
-            issued = i;
+            *s_issued = i;
         }
     } else if (warp == 2) {
         if (lane == 0) {
@@ -174,6 +175,7 @@ __global__ void __launch_bounds__(kRmThreads, 1) pf_router_mma_kernel(const __gr
             }
             umma::commit(mdone);
             mbar_drain(mdone, 0u, globaltimer());
+            if (*s_abort) drain_ring(full, kRmStages, s_issued);
         }
     } else if (warp >= 4) {
         // epilogue: lane quadrant (warp - 4), lane = expert row of the tile
@@ -220,7 +222,6 @@ __global__ void __launch_bounds__(kRmThreads, 1) pf_router_mma_kernel(const __gr
     }
     umma::fence_before();
     __syncthreads();
-    if (warp == 1 && lane == 0 && *s_abort) drain_ring(full, kRmStages, issued);
     if (warp == 0) {
         umma::fence_after();
         umma::tmem_dealloc(tbase, kCols);

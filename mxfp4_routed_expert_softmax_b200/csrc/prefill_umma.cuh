@@ -87,6 +87,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) pf_expert_kernel(const __grid_c
     uint64_t *mdone = mempty + kPfSlots;  // every MMA this CTA issued has completed
     uint32_t *tslot = reinterpret_cast<uint32_t *>(mdone + 1);
     volatile int *s_abort = reinterpret_cast<volatile int *>(tslot + 1);
+    volatile int *s_issued = s_abort + 1;  // stages filled, once all are; -1 before
     PfSlot *slots = reinterpret_cast<PfSlot *>(smem + nst * SB + 512);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Layout &L = p.L;
@@ -108,6 +109,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) pf_expert_kernel(const __grid_c
         mbar_init(mdone, 1);
         fence_mbar_init();
         *s_abort = 0;
+        *s_issued = -1;
     }
     constexpr uint32_t kCols = 512u;
     if (warp == 0) umma::tmem_alloc(tslot, kCols);
@@ -147,7 +149,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) pf_expert_kernel(const __grid_c
         if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&mempty[q % kPfSlots])) : "memory");
     };
 
-    int issued = 0;  // stages filled (the copying warp)
     if (warp == 10) {
         // ---------------------------------------------- group descriptions --
         // Two items in flight: the record of item q+2 and the pairs of item
@@ -266,7 +267,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) pf_expert_kernel(const __grid_c
             }
             slot_done(q);
         }
-        issued = it_stage;
+        if (lane == 0) *s_issued = it_stage;
     } else if (warp >= 4 && warp < 8) {
         // --------------------------------------- scale factors -> TMEM --
         const uint32_t lb = umma::lane_base(warp);
@@ -497,6 +498,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) pf_expert_kernel(const __grid_c
         if (umma::elect()) {
             umma::commit(mdone);
             mbar_drain(mdone, 0u, globaltimer());
+            if (*s_abort) drain_ring(full, nst, s_issued);
         }
     } else {
         // --------------------------------------------------- epilogue --
@@ -630,7 +632,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) pf_expert_kernel(const __grid_c
     }
     umma::fence_before();
     __syncthreads();
-    if (warp == 8 && lane == 0 && *s_abort) drain_ring(full, nst, issued);
     if (warp == 0) {
         umma::fence_after();
         umma::tmem_dealloc(tbase, kCols);

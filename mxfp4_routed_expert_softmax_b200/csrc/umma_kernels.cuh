@@ -318,6 +318,7 @@ __global__ void __launch_bounds__(kUThreads, 1) umma_expert_kernel(const __grid_
     volatile int *s_abort = reinterpret_cast<volatile int *>(tslot + 1);
     volatile int *s_last = s_abort + 1;
     volatile int *s_U = s_last + 1;
+    volatile int *s_issued = s_U + 1;  // stages filled, once all are; -1 before
     const uint8_t **s_blob = reinterpret_cast<const uint8_t **>(smem + nst * SB + kUBarBytes);
     int32_t *s_eid = reinterpret_cast<int32_t *>(s_blob + kMetaU);
     float *s_wu = reinterpret_cast<float *>(s_eid + kMetaU);  // [u][t]
@@ -339,6 +340,7 @@ __global__ void __launch_bounds__(kUThreads, 1) umma_expert_kernel(const __grid_
         mbar_init(mdone, 1);
         fence_mbar_init();
         *s_abort = 0;
+        *s_issued = -1;
     }
     constexpr uint32_t kCols = 512u;
     if (warp == 0) umma::tmem_alloc(tslot, kCols);
@@ -545,7 +547,6 @@ __global__ void __launch_bounds__(kUThreads, 1) umma_expert_kernel(const __grid_
         return y;
     };
 
-    int issued = 0;  // stages filled (the copying warp)
     if (warp == 8) {
         // ------------------------------------------------ TMA producer --
         // Warp-uniform loops, one elected lane issues (as the MMA warp): with
@@ -666,7 +667,7 @@ __global__ void __launch_bounds__(kUThreads, 1) umma_expert_kernel(const __grid_
             pdl_wait();
             if (lane == 0) hdr->prep_done = 0u;
         }
-        issued = it;
+        if (lane == 0) *s_issued = it;
     } else if (warp >= 4 && warp < 8) {
         // --------------------------------------- scale factors -> TMEM --
         const uint32_t lb = umma::lane_base(warp);
@@ -902,6 +903,7 @@ __global__ void __launch_bounds__(kUThreads, 1) umma_expert_kernel(const __grid_
         if (umma::elect()) {
             umma::commit(mdone);
             mbar_drain(mdone, 0u, globaltimer());
+            if (*s_abort) drain_ring(full, nst, s_issued);
         }
     } else if (warp < 4) {
         // --------------------------------------------------- epilogue --
@@ -1084,7 +1086,6 @@ __global__ void __launch_bounds__(kUThreads, 1) umma_expert_kernel(const __grid_
     }
     umma::fence_before();
     __syncthreads();
-    if (warp == 8 && lane == 0 && *s_abort) drain_ring(full, nst, issued);
     if (warp == 0) {
         umma::fence_after();
         umma::tmem_dealloc(tbase, kCols);
