@@ -480,8 +480,8 @@ k3moe_status k3moe_device_status(void *ws, void *stream);
  *           "routing loaded" signal that is never given, so its waits run
  *           out and the call records K3MOE_ERR_DEVICE_TIMEOUT (the kernels
  *           then finish early with undefined outputs; nothing faults);
- *           k3moe_linear leaves out a copy of its last reduction step, with
- *           the same end.
+ *           k3moe_linear leaves out some of the copies it waits for, with the
+ *           same end.
  * wait_limit_ns bounds every device wait of later calls (0: the default of
  * 2 seconds).  Returns K3MOE_ERR_INVALID_ARGUMENT for an unknown mode.
  */

@@ -136,6 +136,14 @@ k3moe_status device_info(DeviceInfo **out) {
         if (r == cudaSuccess) r = set_smem(linear_stream_kernel<2, false, 2>, big);
         if (r == cudaSuccess) r = set_smem(linear_stream_kernel<2, true, 1>, big);
         if (r == cudaSuccess) r = set_smem(linear_stream_kernel<2, true, 2>, big);
+        if (r == cudaSuccess) r = set_smem(linear_stream_kernel<1, false, 1, true>, big);
+        if (r == cudaSuccess) r = set_smem(linear_stream_kernel<1, false, 2, true>, big);
+        if (r == cudaSuccess) r = set_smem(linear_stream_kernel<1, true, 1, true>, big);
+        if (r == cudaSuccess) r = set_smem(linear_stream_kernel<1, true, 2, true>, big);
+        if (r == cudaSuccess) r = set_smem(linear_stream_kernel<2, false, 1, true>, big);
+        if (r == cudaSuccess) r = set_smem(linear_stream_kernel<2, false, 2, true>, big);
+        if (r == cudaSuccess) r = set_smem(linear_stream_kernel<2, true, 1, true>, big);
+        if (r == cudaSuccess) r = set_smem(linear_stream_kernel<2, true, 2, true>, big);
         for (int i = 0; i < 8 && r == cudaSuccess; ++i) r = set_smem(linear_tile_variant(i & 1, i & 2, i & 4), big);
         for (int i = 0; i < 8 && r == cudaSuccess; ++i) r = set_smem(linear_pair_variant<false>(i & 1, i & 2, i & 4), big);
         for (int i = 0; i < 8 && r == cudaSuccess; ++i) r = set_smem(linear_pair_variant<true>(i & 1, i & 2, i & 4), big);
@@ -937,8 +945,9 @@ k3moe_status launch_stream(const DeviceInfo &di, LinearStreamParams &a, cudaStre
     if (s == K3MOE_OK) s = tmap_bf16_rows(p.x, p.K, p.T, a.tx, p.ldx, p.T, a.kc);
     if (s != K3MOE_OK) return s;
     cudaError_t e =
-        launch(linear_stream_kernel<RG, GATED, TG>, dim3(ctas), dim3(32 * kLsWarps),
-                  (size_t)ls_smem_bytes(NM, TG, a.kc, a.ns), st, true, a);
+        launch(g_fault_mode.load(std::memory_order_relaxed) ? linear_stream_kernel<RG, GATED, TG, true>
+                                                            : linear_stream_kernel<RG, GATED, TG>,
+               dim3(ctas), dim3(32 * kLsWarps), (size_t)ls_smem_bytes(NM, TG, a.kc, a.ns), st, true, a);
     return e == cudaSuccess ? K3MOE_OK : cuda_fail(e, "linear launch");
 }
 template <int RG, bool GATED>
@@ -967,7 +976,6 @@ k3moe_status linear_launch(const LinearParams &p, WsHeader *hdr, cudaStream_t st
         a.p = p;
         a.hdr = hdr;
         a.wait_ns = wait_limit();
-        a.inject = g_fault_mode.load(std::memory_order_relaxed);
         return linear_stream(*di, a, st);
     }
     cudaError_t e;
@@ -975,7 +983,7 @@ k3moe_status linear_launch(const LinearParams &p, WsHeader *hdr, cudaStream_t st
     a.p = p;
     a.hdr = hdr;
     a.wait_ns = wait_limit();
-    a.inject = g_fault_mode.load(std::memory_order_relaxed);
+    const int inject = g_fault_mode.load(std::memory_order_relaxed) << 8;  // in a.nst
     const int nkt = ceil_div(p.K, kLtKStep);
     // The variant of the least estimated time, in us as measured on B200.  A
     // K-step of a tile takes what an SM takes in (64 bytes a clock) and a
@@ -1052,6 +1060,7 @@ k3moe_status linear_launch(const LinearParams &p, WsHeader *hdr, cudaStream_t st
         a.nst = std::min((room - kLpExch) / sb, kLtMaxStages);
         const int pairs = (int)std::min<long long>(di->pairs, (long long)a.nrb * a.ntt);
         const size_t bytes = 1024 + kLtHead + a.nst * sb + kLpExch;
+        a.nst |= inject;
         a.chain = kLtChain;
         const auto variant = p.out_fp32 ? linear_pair_variant<true> : linear_pair_variant<false>;
         e = launch_cluster(variant(gated, p.resid != nullptr, p.vec != 0), 2 * pairs, kLpThreads, bytes, 2, st, a);
@@ -1065,6 +1074,7 @@ k3moe_status linear_launch(const LinearParams &p, WsHeader *hdr, cudaStream_t st
     const int red = a.split > 1 ? a.split * ceil_div(a.bn, a.split) * 512 : 0, part = a.bn * 512;
     a.nst = std::min({(room - red - (apart ? part : 0)) / sb, kLtMaxStages, std::max(steps, 2)});
     const int stages = std::max(a.nst * sb, apart ? 0 : part);
+    a.nst |= inject;
     a.part = kLtHead + (apart ? stages : 0);
     a.red = kLtHead + stages + (apart ? part : 0);
     a.tcols = 32;

@@ -186,7 +186,6 @@ struct LinearStreamParams {
     int kc, ns;  // columns per chunk (a multiple of 64), stages per warp
     WsHeader *hdr;
     uint64_t wait_ns;
-    int inject;  // failure-path tests: the copies of one last step are never made
 };
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -205,7 +204,9 @@ __host__ __device__ constexpr int ls_smem_bytes(int nm, int tg, int kc, int ns) 
 }
 
 // RG: groups of 8 output columns per CTA.
-template <int RG, bool GATED, int TG>
+// INJECT: failure-path tests, one warp makes no copies (a kernel of its own: a
+// parameter for it cost 0.05 to 0.2 us at the start).
+template <int RG, bool GATED, int TG, bool INJECT = false>
 __global__ void __launch_bounds__(32 * kLsWarps) linear_stream_kernel(const __grid_constant__ LinearStreamParams a) {
     constexpr int NM = RG * (GATED ? 2 : 1), TT = 8 * TG;
     extern __shared__ __align__(128) uint8_t ls_raw[];
@@ -234,10 +235,9 @@ __global__ void __launch_bounds__(32 * kLsWarps) linear_stream_kernel(const __gr
     const int chunks = ceil_div(p.K, a.kc), groups = ceil_div(p.N, RG * 8);
     // The warp's next chunk to copy: it runs on into the CTA's next groups of
     // columns while the sums of one are brought together.
-    int ig = warp < chunks ? blockIdx.x : groups, ic = warp, issued = 0;
+    int ig = warp < chunks && !(INJECT && warp == 0) ? blockIdx.x : groups, ic = warp, issued = 0;
     auto issue = [&](int s) {
         if (ig >= groups) return;
-        if (a.inject && warp == 0 && ic + kLsWarps >= chunks && ig + gridDim.x >= groups) return;
         if (umma::elect()) {
             uint8_t *st = ring + s * stageb;
             mbar_arrive_expect_tx(&bar[s], (uint32_t)((NM * 8 + T) * rowb));  // the other token rows stay as they are
@@ -365,7 +365,8 @@ struct LinearTcParams {
     LinearParams p;
     int bn;          // tokens per tile (pair kernel: of the pair)
     int whole, parts;  // pair kernel: tiles run whole (the first ones); parts of bn / parts tokens of each other tile
-    int nst;         // pipeline stages
+    int nst;         // pipeline stages; from bit 8: failure-path tests, last K-steps that one CTA does not copy
+                     // (with a parameter of its own 333 x 1001 x 1000 took 8.30 us, so 8.19)
     int nrb, ntt;    // row blocks, token tiles
     int split;       // tile kernel: CTAs (one cluster) that share a tile's K
     int chain;       // K-steps accumulated in tensor memory at a stretch (pair kernel: of an fp32 output)
@@ -373,7 +374,6 @@ struct LinearTcParams {
     int part, red;   // tile kernel: offsets of its own sums and of the other CTAs' parts
     WsHeader *hdr;
     uint64_t wait_ns;
-    int inject;  // failure-path tests: the copies of one last step are never made
 };
 
 // A tile of 128 weight rows x bn tokens per cluster of `split` CTAs, which
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const LinearParams &p = a.p;
-    const int nst = a.nst, bn = a.bn, S = a.split;
+    const int nst = a.nst & 255, bn = a.bn, S = a.split;
     const int SB = kLtA + bn * 128;
     uint64_t *full = reinterpret_cast<uint64_t *>(smem);
     uint64_t *empty = full + nst;
@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
     const int n0 = (tile % a.nrb) * nrow, t0 = (tile / a.nrb) * bn;
     const int nkt = ceil_div(p.K, kLtKStep);
     const int kt0 = (int)((long long)nkt * rank / S), nk = (int)((long long)nkt * (rank + 1) / S) - kt0;
-    const int fill = a.inject && rank == 0 ? nk - 1 : nk;  // K-steps copied
+    const int fill = rank == 0 ? nk - (a.nst >> 8) : nk;  // K-steps copied
     const int nch = ceil_div(nk, a.chain);
     const int cpo = ceil_div(bn, S);  // columns that one CTA of the cluster finishes
     auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait_warp(bar, parity, a.hdr, a.wait_ns, s_abort); };
@@ -702,7 +702,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const LinearParams &p = a.p;
-    const int nst = a.nst, bn = a.bn;
+    const int nst = a.nst & 255, bn = a.bn;
     const int SB = kLtA + bn * 64;
     uint64_t *full = reinterpret_cast<uint64_t *>(smem);
     uint64_t *empty = full + nst;
@@ -772,7 +772,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) linear_pair_kernel(const __grid
             int n0, t0;
             const int tn = tile_at(it, n0, t0), tx = t0 + rank * (tn / 2);
             const void *xmap = it < a.whole ? a.tx : a.tx_part;
-            const int fill = a.inject && rank == 1 && it + pairs >= items ? nk - 1 : nk;
+            const int fill = rank == 1 && it + pairs >= items ? nk - (a.nst >> 8) : nk;
             for (int kt = 0; kt < fill; ++kt, ++i) {
                 if (!wait(&empty[s], ph)) {
                     ok = false;

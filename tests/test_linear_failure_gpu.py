@@ -1,6 +1,6 @@
 """Waits of the dense product that run out, without any GPU fault: the
-library's failure-path hook leaves out a copy of the last reduction step.  The
-call records K3MOE_ERR_DEVICE_TIMEOUT and ends in bounded time with nothing of
+library's failure-path hook leaves out some of the copies waited for.  The call
+records K3MOE_ERR_DEVICE_TIMEOUT and ends in bounded time with nothing of
 its own in flight, the device stays usable, and on a workspace zero-filled
 again the next call gives the bytes from before the failure."""
 import time
