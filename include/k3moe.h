@@ -357,7 +357,13 @@ k3moe_status k3moe_layer_routed(const void *x, int32_t T, const int32_t *idx, co
  *   g[t][n]   = sum_k x[t][k] w_gate[n][k] + bias_gate[n]
  * act: K3MOE_ACT_NONE, _RELU, _SILU (v / (1 + exp(-v))), _GELU (v times the
  * normal distribution function of v), _GELU_TANH (its tanh approximation).
- * Products are exact, sums and the epilogue fp32, one rounding at the end.
+ * Products are exact, sums and the epilogue fp32, one rounding at the end.  The
+ * tensor cores cut the running sum towards zero after every 16 products, by at
+ * most 2^-23 of it.  With an fp32 output, and for up to 8 tokens, chains of 512
+ * columns or fewer are added rounding to nearest: within 8e-6 of the sum of the
+ * terms' sizes (1.3e-6 measured).  With a bf16 output of more tokens one chain
+ * may have up to 32768 columns: measured up to 3e-5 of that sum for k = 7168
+ * and 2e-4 for 32768 (half a step of bf16 is 2e-3 to 4e-3).
  * One launch; the variant (and with it the order of the sums) depends on T, n,
  * k, the gate and the output's type, never on the values.
  *

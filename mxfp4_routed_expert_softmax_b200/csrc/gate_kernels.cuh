@@ -147,12 +147,14 @@ __device__ __noinline__ void gate_exact(const GateParams &p, long long t, GateEx
 // Weights are 32-bit: the scores of the picks from expf, the softmax's argument
 // l - max with its rounding error carried along.
 //
-// Bound by instruction issue: about 1000 instructions a token of 896 experts
-// (3.6 kB), so 4096 tokens, softmax, top 16, take 6.6 us where their bytes take
-// 2.3 (8.0 us with a compare and a store per logit, 45 us with a warp-wide
-// maximum per pick over 64-bit values in shared memory).  8191 tokens, sigmoid
-// with a bias: 14.8 us (4.6), of which one in some hundred tokens needs 64
-// bits.  A single token: 3.0 us, the chain of the steps above.
+// Bound by one wave's load and chain of steps as much as by instruction issue:
+// about 1000 instructions a token of 896 experts (3.6 kB), half of the issue
+// slots filled, so 4096 tokens, softmax, top 16, take 6.7 us where their
+// instructions take 3.5 and their bytes 2.3 (8.0 us with a compare and a store
+// per logit, 45 us with a warp-wide maximum per pick over 64-bit values in
+// shared memory).  8191 tokens, sigmoid with a bias: 15.5 us (bytes 4.6), of
+// which one in some hundred tokens needs 64 bits.  A single token: 3.0 us, the
+// chain of the steps above.
 constexpr int kGateWarps = 4;
 constexpr int kGateCap = 160;  // a multiple of 8
 struct alignas(16) GateWarp {

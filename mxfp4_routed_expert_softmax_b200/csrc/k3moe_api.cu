@@ -923,8 +923,9 @@ cudaError_t launch_cluster(Kern kernel, int grid, int block, size_t smem, int n,
 // four stages per warp, all of K where they hold it.  Up to 8 tokens: two CTAs
 // per SM at most, which go from group to group of columns (one streams while
 // the other starts or ends a group): 8 x 7168 x 7168 in 19 us, 27 with a CTA
-// per group.  More tokens: their stages are too large for that (16 x 7168 x
-// 7168: 48 us, against 27 with a CTA per group, as many per SM as fit).
+// per group.  More tokens: a CTA per group, up to four per SM as they fit,
+// since their larger stages leave a CTA fewer (12 x 7168 x 1536 with a residual
+// 6.2 us, 8.1 going from group to group; 16 x 2600 x 7168 14.7, 14.1).
 template <int RG, bool GATED, int TG>
 k3moe_status launch_stream(const DeviceInfo &di, LinearStreamParams &a, cudaStream_t st) {
     constexpr int NM = RG * (GATED ? 2 : 1);

@@ -173,7 +173,7 @@ __device__ __forceinline__ void linear_bias(const float *bias, int n, int dn, in
 // registers, 8 lines each: one token's 896 x 7168 took 4.4 us to arrive; bulk
 // copies of 512-byte rows: 4.7 us; this: 3.3 us.)  Bound by memory where K and n
 // are large (7168 x 7168: 19 us, 5.4 TB/s), by latency below (4 tokens, 680 x
-// 680: 2.1 us).
+// 680: 2.1 us in a captured graph).
 constexpr int kLsMaxT = 16;
 constexpr int kLsWarps = 8;
 constexpr int kLsMaxStages = 4;
@@ -388,8 +388,13 @@ struct LinearTcParams {
 // with fp32 outputs the sum moves to shared memory (tiles of more than 128
 // tokens: registers) every `chain` K-steps (two tensor-memory buffers) and the
 // pieces are added there, rounded to nearest.
-// A step of 16 costs about 2^-27 of the sum (measured over 1344 steps), so a
-// bf16 output, whose half step is 2^-9, takes chains of up to 16384 columns.
+// A step of 16 cuts up to 2^-23 of it, towards zero.  Measured against 64 bits:
+// chains of 8 K-steps 0.9e-6 of a sum of equal signs and 0.5e-6 (rms) of the
+// outputs' size at random signs, whatever K; one chain of 7168 columns 2.8e-5
+// and 0.8e-5, of 32768 1.8e-4 and 3.8e-5.  A bf16 output's half step is 2e-3 to
+// 4e-3 of it, so it takes chains of up to kLtChainBf16 K-steps here (16384
+// columns; K in S parts is in S chains), of kLpMaxSteps in the pair kernel
+// (32768).
 template <bool GATED, bool RESID, bool OUT32>
 __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid_constant__ LinearTcParams a) {
     extern __shared__ uint8_t smem_raw[];
@@ -660,9 +665,10 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tile_kernel(const __grid
 // the MMA work of a single CTA's tile.  Two tensor-memory buffers: the
 // epilogue of a tile runs under the next tile's MMAs.  Bound by the tensor
 // cores under the power limit, and by whole waves of tiles: 4096 tokens x 7168 x
-// 7168 at 1.46 PFLOP/s, gated 4096 x 1536 x 7168 at 1.42, 4095 x 7168 x 1536 with
-// a residual at 1.28.  Issue loops that keep one lane in a branch (without
-// elect) ran the MMAs at two thirds of that.  fp32 outputs: the chains of the
+// 7168 at 1.30 to 1.46 PFLOP/s, gated 4096 x 1536 x 7168 at 1.21 to 1.28, 4095 x
+// 7168 x 1536 with a residual at 1.00 to 1.06 in calls that follow one another
+// for a second, at 1.25 in runs of some 10 ms.  Issue loops that keep one lane
+// in a branch (without elect) ran the MMAs at two thirds of that.  fp32 outputs: the chains of the
 // tile kernel, a buffer each, added in the epilogue warps' registers; a tile's
 // end then covers two chains of the next tile, not all of it (4096 x 7168 x 1536
 // with a residual 131 us, 4096 x 7168 x 7168 360 us).
