@@ -936,11 +936,12 @@ __global__ void __launch_bounds__(kLThreads, 1) layer_kernel(const __grid_consta
                     }
                 }
             }
-            if (npend > 0) {
-                // after a wait that gave up too: the stages have to fill
-                if (!*s_abort) gu_ready(true);
+            if (npend > 0 && !*s_abort && gu_ready(true)) {
                 for (int q = 0; q < npend; ++q) issue_b(pend_s[q], decode(3, pend_unit[q]));
                 npend = 0;
+            }
+            if (*s_abort) {  // the stages have to fill, or they cannot be drained
+                for (int q = 0; q < npend; ++q) issue_b(pend_s[q], decode(3, pend_unit[q]));
             }
             *s_issued = i;
         }

@@ -3,6 +3,8 @@ library's failure-path hook withholds the signal that the routing is loaded.
 The roles of a CTA that go through barriers together leave together, so the
 call ends, records K3MOE_ERR_DEVICE_TIMEOUT, and on a workspace zero-filled
 again gives the same bytes as before."""
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -63,3 +65,35 @@ def test_waits_that_run_out(cfg, T):
         got, status = run()
         assert status == m.K3MOE_OK
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("T", [1, 5])
+@pytest.mark.parametrize("cfg", [k3gen.CONFIGS["tiny"], CFGS[0], CFGS[2]], ids=lambda c: c.name)
+def test_one_launch_waits_that_run_out(cfg, T):
+    """The decode pass as one launch: the same end, well before the limit of a
+    drain (2 s)."""
+    W = kdev.weights(cfg)
+    inp = kdev.DeviceInputs(cfg, T=T)
+    dims = dims_of(cfg, m.K3MOE_OUT_FP32 | m.K3MOE_ONE_LAUNCH)
+    ws = m.new_workspace(dims, T)
+
+    def run():
+        y = torch.zeros((T, cfg.d), device="cuda")
+        m.check(m.k3moe_layer(inp.x, T, W.w_router, None, W.blob_ptrs, *W.shared, dims, y, None, None, ws))
+        torch.cuda.synchronize()
+        return y, m.k3moe_device_status(ws)
+
+    want, status = run()
+    assert status == m.K3MOE_OK
+    t0 = time.monotonic()
+    try:
+        assert m.k3moe_debug_set_fault(1, 1_000_000) == m.K3MOE_OK
+        _, status = run()
+    finally:
+        m.k3moe_debug_set_fault(0, 0)
+    assert status == m.K3MOE_ERR_DEVICE_TIMEOUT
+    assert time.monotonic() - t0 < 1.0
+    ws.zero_()
+    got, status = run()
+    assert status == m.K3MOE_OK
+    assert torch.equal(got, want)
